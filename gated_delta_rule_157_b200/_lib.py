@@ -95,9 +95,32 @@ class GateArgs(ctypes.Structure):
     ]
 
 
+class PackedArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("N", "T", "P", "H", "HV", "Dk", "Dv", "max_seqlen", "dtype", "algo")] + \
+        [(n, ctypes.c_float) for n in ("g_min", "scale", "l2_eps")] + \
+        [(n, ctypes.c_int) for n in ("qk_l2norm_in_kernel", "beta_sigmoid_in_kernel", "gate_in_kernel",
+                                     "g_per_head")] + \
+        [(n, ctypes.c_longlong) for n in ("ld_q", "ld_k", "ld_v", "ld_g", "ld_beta", "ld_o")] + \
+        [(n, ctypes.c_void_p) for n in ("q", "k", "v", "g", "beta", "A_log", "dt_bias", "cu_seqlens", "slots",
+                                        "fresh", "pool", "o")]
+
+
+class PackedConvArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("N", "T", "P", "C", "K", "head_dim", "silu", "dtype")] + \
+        [("l2_eps", ctypes.c_float), ("ld_x", ctypes.c_longlong), ("ld_y", ctypes.c_longlong)] + \
+        [(n, ctypes.c_void_p) for n in ("x", "w", "bias", "cu_seqlens", "slots", "fresh", "pool", "y")]
+
+
+class GroupNormArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("N", "L", "C", "G", "act", "dtype")] + [("eps", ctypes.c_float)] + \
+        [(n, ctypes.c_void_p) for n in ("x", "gate", "weight", "bias", "y", "mean", "rstd", "dy", "dx", "dgate",
+                                        "dweight", "dbias", "workspace")]
+
+
 EXPORTS = ["kda_chunk_fwd", "kda_chunk_bwd", "kda_step", "kda_compose", "kda_device_status",
            "kda_status_string", "kda_version", "kda_debug_chunk_stall",
-           "kda_short_conv", "kda_output_gate"]
+           "kda_short_conv", "kda_output_gate", "kda_packed_fwd", "kda_packed_conv",
+           "kda_group_norm_workspace", "kda_group_norm_fwd", "kda_group_norm_bwd"]
 
 _lib = None
 
@@ -125,6 +148,12 @@ def load():
     lib.kda_short_conv.restype = ctypes.c_int
     lib.kda_output_gate.argtypes = [ctypes.POINTER(GateArgs), ctypes.c_void_p]
     lib.kda_output_gate.restype = ctypes.c_int
+    for name, args in (("kda_packed_fwd", PackedArgs), ("kda_packed_conv", PackedConvArgs),
+                       ("kda_group_norm_fwd", GroupNormArgs), ("kda_group_norm_bwd", GroupNormArgs)):
+        getattr(lib, name).argtypes = [ctypes.POINTER(args), ctypes.c_void_p]
+        getattr(lib, name).restype = ctypes.c_int
+    lib.kda_group_norm_workspace.argtypes = [ctypes.c_int] * 6
+    lib.kda_group_norm_workspace.restype = ctypes.c_ulonglong
     lib.kda_step.argtypes = [ctypes.POINTER(StepArgs), ctypes.c_void_p]
     lib.kda_step.restype = ctypes.c_int
     lib.kda_compose.argtypes = [ctypes.c_int] * 4 + [ctypes.c_void_p] * 5
@@ -428,6 +457,206 @@ def kda_output_gate(o, gate, weight=None, *, eps=1e-6, y=None, stream=None):
     a.o, a.gate, a.weight, a.y = _ptr(o), _ptr(gate), _ptr(weight), _ptr(y)
     _call("kda_output_gate", dev, lib.kda_output_gate, ctypes.byref(a), _stream(stream, dev))
     return y
+
+
+def _check_rows(t, name, shape, dtype, device):
+    """As _check, for rows that may lie apart: every dimension but the first
+    contiguous.  Returns the elements from one row to the next."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if t.dtype != dtype:
+        raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
+    row = 1
+    for d in shape[1:]:
+        row *= d
+    if t.numel() and not t[0].is_contiguous():
+        raise ValueError("the rows of %s must be contiguous" % name)
+    if shape[0] <= 1 or t.numel() == 0:
+        return row
+    if t.stride(0) < row:
+        raise ValueError("the rows of %s overlap" % name)
+    return t.stride(0)
+
+
+def _check_packing(cu_seqlens, slots, fresh, rows, dev):
+    """Checks the arrays of a packed batch; returns its number of sequences."""
+    n = rows
+    if cu_seqlens is not None:
+        if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+            raise ValueError("cu_seqlens must be a tensor [N + 1]")
+        n = cu_seqlens.numel() - 1
+        _check(cu_seqlens, "cu_seqlens", (n + 1,), torch.int32, dev)
+    _check(slots, "slots", (n,), torch.int32, dev)
+    if fresh is not None and isinstance(fresh, torch.Tensor) and fresh.dtype == torch.bool:
+        fresh = fresh.view(torch.uint8)
+    _check(fresh, "fresh", (n,), torch.uint8, dev)
+    return n, fresh
+
+
+def kda_packed_fwd(q, k, v, g, beta, pool, *, cu_seqlens=None, slots=None, fresh=None, max_seqlen=None,
+                   A_log=None, dt_bias=None, g_min=-5.0, scale=1.0, l2_eps=1e-6, qk_l2norm_in_kernel=True,
+                   beta_sigmoid_in_kernel=True, gate_in_kernel=True, g_per_head=False, algo="auto", o=None,
+                   stream=None):
+    """The delta rule over a packed batch of N sequences, states in a pool of
+    slots updated in place.  Returns o [T,HV,Dv].
+
+    q, k [T,H,Dk]; v [T,HV,Dv]; g [T,HV,Dk] ([T,HV] with g_per_head); beta
+    [T,HV] -- all float32 or all bfloat16; views whose rows lie apart are taken
+    as they are.  pool [P,HV,Dk,Dv] float32.  cu_seqlens [N+1] int32 row bounds
+    (None: every row is a sequence, a decode step); slots [N] int32 (None:
+    sequence s has slot s; negative: the sequence is skipped, its rows of o left
+    as they were); fresh [N] uint8 or bool: start from a zero state.  max_seqlen:
+    the longest length if known (None: unknown), picks kernels only.  algo:
+    "auto", "simt" (recurrence, fp32) or "tc" (chunks on the tensor cores: bf16,
+    Dk = Dv = 128, g_per_head).  The other arguments as kda_chunk_fwd.
+
+    The arrays are read on the device: bounds outside [0, T], a slot >= P or one
+    that an earlier sequence names make the sequence skipped and reported by
+    kda_device_status.
+    """
+    lib = load()
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor")
+    dev, dt = q.device, q.dtype
+    T, H, Dk = q.shape
+    P, HV, _, Dv = pool.shape
+    gk = () if g_per_head else (Dk,)
+    a = PackedArgs()
+    a.dtype = _dtype_code(q)
+    a.ld_q = _check_rows(q, "q", (T, H, Dk), dt, dev)
+    a.ld_k = _check_rows(k, "k", (T, H, Dk), dt, dev)
+    a.ld_v = _check_rows(v, "v", (T, HV, Dv), dt, dev)
+    a.ld_g = _check_rows(g, "g", (T, HV) + gk, dt, dev)
+    a.ld_beta = _check_rows(beta, "beta", (T, HV), dt, dev)
+    _check(pool, "pool", (P, HV, Dk, Dv), torch.float32, dev)
+    _check(A_log, "A_log", (HV,), torch.float32, dev)
+    _check(dt_bias, "dt_bias", (HV,) + gk, torch.float32, dev)
+    n, fresh = _check_packing(cu_seqlens, slots, fresh, T, dev)
+    if o is None:
+        o = torch.empty((T, HV, Dv), dtype=dt, device=dev)
+    a.ld_o = _check_rows(o, "o", (T, HV, Dv), dt, dev)
+    a.N, a.T, a.P, a.H, a.HV, a.Dk, a.Dv = n, T, P, H, HV, Dk, Dv
+    a.max_seqlen, a.algo = int(max_seqlen or 0), ALGOS[algo]
+    a.g_min, a.scale, a.l2_eps = float(g_min), float(scale), float(l2_eps)
+    a.qk_l2norm_in_kernel = int(bool(qk_l2norm_in_kernel))
+    a.beta_sigmoid_in_kernel = int(bool(beta_sigmoid_in_kernel))
+    a.gate_in_kernel = _gate_code(gate_in_kernel)
+    a.g_per_head = int(bool(g_per_head))
+    a.q, a.k, a.v, a.g, a.beta = map(_ptr, (q, k, v, g, beta))
+    a.A_log, a.dt_bias = _ptr(A_log), _ptr(dt_bias)
+    a.cu_seqlens, a.slots, a.fresh = _ptr(cu_seqlens), _ptr(slots), _ptr(fresh)
+    a.pool, a.o = _ptr(pool), _ptr(o)
+    _call("kda_packed_fwd", dev, lib.kda_packed_fwd, ctypes.byref(a), _stream(stream, dev))
+    return o
+
+
+def kda_packed_conv(x, w, pool, bias=None, *, cu_seqlens=None, slots=None, fresh=None, head_dim=0, silu=True,
+                    l2_eps=1e-6, y=None, stream=None):
+    """kda_short_conv over a packed batch: x [T,C] float32 or bfloat16 (C % 128
+    == 0, rows may lie apart), w [C,K], bias [C] float32; pool [P,K-1,C] of x's
+    type holds each slot's window and is updated in place.  cu_seqlens, slots
+    and fresh as kda_packed_fwd.  Returns y [T,C]."""
+    lib = load()
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    dev, dt = x.device, x.dtype
+    T, C = x.shape
+    K, P = w.shape[1], pool.shape[0]
+    a = PackedConvArgs()
+    a.dtype = _dtype_code(x)
+    a.ld_x = _check_rows(x, "x", (T, C), dt, dev)
+    _check(w, "w", (C, K), torch.float32, dev)
+    _check(bias, "bias", (C,), torch.float32, dev)
+    _check(pool, "pool", (P, K - 1, C), dt, dev)
+    n, fresh = _check_packing(cu_seqlens, slots, fresh, T, dev)
+    if y is None:
+        y = torch.empty((T, C), dtype=dt, device=dev)
+    a.ld_y = _check_rows(y, "y", (T, C), dt, dev)
+    a.N, a.T, a.P, a.C, a.K = n, T, P, C, K
+    a.head_dim, a.silu, a.l2_eps = int(head_dim), int(bool(silu)), float(l2_eps)
+    a.x, a.w, a.bias = _ptr(x), _ptr(w), _ptr(bias)
+    a.cu_seqlens, a.slots, a.fresh = _ptr(cu_seqlens), _ptr(slots), _ptr(fresh)
+    a.pool, a.y = _ptr(pool), _ptr(y)
+    _call("kda_packed_conv", dev, lib.kda_packed_conv, ctypes.byref(a), _stream(stream, dev))
+    return y
+
+
+ACTS = {"none": 0, "silu": 1, "sigmoid": 2}
+
+
+def _group_norm_args(x, groups, weight, bias, gate, act):
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    N, L, C = x.shape
+    dev, dt, G = x.device, x.dtype, int(groups)
+    if act not in ACTS:
+        raise ValueError("act must be one of %s" % ", ".join(ACTS))
+    if G < 1 or C % G:
+        raise ValueError("%d channels do not divide into %d groups" % (C, G))
+    _check(x, "x", (N, L, C), dt, dev)
+    _check(gate, "gate", (N, L, C), dt, dev)
+    _check(weight, "weight", (C,), torch.float32, dev)
+    _check(bias, "bias", (C,), torch.float32, dev)
+    a = GroupNormArgs()
+    a.N, a.L, a.C, a.G, a.act, a.dtype = N, L, C, G, ACTS[act], _dtype_code(x)
+    a.x, a.gate, a.weight, a.bias = _ptr(x), _ptr(gate), _ptr(weight), _ptr(bias)
+    return a
+
+
+def _group_norm_workspace(lib, a, backward, dev):
+    n = int(lib.kda_group_norm_workspace(a.N, a.L, a.C, a.G, a.dtype, int(backward)))
+    return torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+
+
+def kda_group_norm_fwd(x, groups, weight=None, bias=None, gate=None, *, act="none", eps=1e-5, y=None, stream=None):
+    """Group norm with an activation over channels-last rows: statistics over
+    the L rows and C / groups channels of each (n, group), then
+    y = act(u), or u * act(gate) with a gate, u = weight * h + bias.
+
+    x, gate [N,L,C] float32 or bfloat16 (L = 1: every row on its own, a token's
+    heads as groups); weight, bias [C] float32.  act: "none", "silu" or
+    "sigmoid".  Returns (y, mean [N,G], rstd [N,G])."""
+    lib = load()
+    a = _group_norm_args(x, groups, weight, bias, gate, act)
+    dev = x.device
+    if y is None:
+        y = torch.empty_like(x)
+    _check(y, "y", tuple(x.shape), x.dtype, dev)
+    mean = torch.empty((a.N, a.G), dtype=torch.float32, device=dev)
+    rstd = torch.empty((a.N, a.G), dtype=torch.float32, device=dev)
+    ws = _group_norm_workspace(lib, a, False, dev)
+    a.eps = float(eps)
+    a.y, a.mean, a.rstd, a.workspace = _ptr(y), _ptr(mean), _ptr(rstd), _ptr(ws)
+    _call("kda_group_norm_fwd", dev, lib.kda_group_norm_fwd, ctypes.byref(a), _stream(stream, dev))
+    return y, mean, rstd
+
+
+def kda_group_norm_bwd(dy, x, groups, mean, rstd, weight=None, bias=None, gate=None, *, act="none", want_dx=True,
+                       want_dgate=True, want_params=True, stream=None):
+    """Gradient of kda_group_norm_fwd with the same arguments, from the mean and
+    rstd it returned.  Returns a dict: dx, dgate in x's type (dgate only with a
+    gate), dweight, dbias [C] float32; None for what is not wanted or not given."""
+    lib = load()
+    a = _group_norm_args(x, groups, weight, bias, gate, act)
+    dev = x.device
+    _check(dy, "dy", tuple(x.shape), x.dtype, dev)
+    _check(mean, "mean", (a.N, a.G), torch.float32, dev)
+    _check(rstd, "rstd", (a.N, a.G), torch.float32, dev)
+    f32 = dict(dtype=torch.float32, device=dev)
+    out = {"dx": torch.empty_like(x) if want_dx else None,
+           "dgate": torch.empty_like(x) if want_dgate and gate is not None else None,
+           "dweight": torch.empty(a.C, **f32) if want_params and weight is not None else None,
+           "dbias": torch.empty(a.C, **f32) if want_params and bias is not None else None}
+    ws = _group_norm_workspace(lib, a, True, dev)
+    a.dy, a.mean, a.rstd, a.workspace = _ptr(dy), _ptr(mean), _ptr(rstd), _ptr(ws)
+    for name, t in out.items():
+        setattr(a, name, _ptr(t))
+    _call("kda_group_norm_bwd", dev, lib.kda_group_norm_bwd, ctypes.byref(a), _stream(stream, dev))
+    return out
 
 
 def kda_device_status(stream=None, device=None):

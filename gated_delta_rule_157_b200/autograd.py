@@ -54,3 +54,28 @@ def kda_chunk(q, k, v, g, beta, *, A_log=None, dt_bias=None, S0=None, chunk=64, 
     if algo not in ("auto", "simt", "tc"):
         raise ValueError("algo must be 'auto', 'simt' or 'tc'")
     return KDAChunkFunction.apply(q, k, v, g, beta, A_log, dt_bias, S0, dict(opts, fwd_algo=algo))
+
+
+class KDAGroupNormFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, gate, groups, act, eps):
+        y, mean, rstd = _lib.kda_group_norm_fwd(x, groups, weight, bias, gate, act=act, eps=eps)
+        ctx.save_for_backward(x, weight, bias, gate, mean, rstd)
+        ctx.groups, ctx.act = groups, act
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, weight, bias, gate, mean, rstd = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        d = _lib.kda_group_norm_bwd(dy.to(x.dtype).contiguous(), x, ctx.groups, mean, rstd, weight, bias, gate,
+                                    act=ctx.act, want_dx=need[0], want_dgate=need[3],
+                                    want_params=need[1] or need[2])
+        return (d["dx"], d["dweight"] if need[1] else None, d["dbias"] if need[2] else None, d["dgate"], None, None,
+                None)
+
+
+def kda_group_norm(x, groups, weight=None, bias=None, gate=None, *, act="none", eps=1e-5):
+    """Differentiable kda_group_norm_fwd: returns y; gradients flow to x,
+    weight, bias and gate through kda_group_norm_bwd."""
+    return KDAGroupNormFunction.apply(x, weight, bias, gate, int(groups), act, float(eps))

@@ -2,7 +2,9 @@
 // dispatch and launch.  Validation errors return before anything is enqueued.
 #include <stdint.h>
 
+#include "kda_group_norm.cuh"
 #include "kda_internal.cuh"
+#include "kda_packed.cuh"
 
 namespace {
 
@@ -326,13 +328,222 @@ kda_status kda_output_gate(const kda_gate_args *a, void *stream) {
     return cuda_status(kda::launch_output_gate(p, static_cast<cudaStream_t>(stream)));
 }
 
+// Rows a strided activation spans: T rows of `row` elements, `ld` apart.
+static size_t span_bytes(long long T, long long ld, size_t row, size_t es) {
+    return T > 0 ? ((size_t)(T - 1) * (size_t)ld + row) * es : 0;
+}
+
+kda_status kda_packed_fwd(const kda_packed_args *a, void *stream) {
+    if (!a) return KDA_ERR_INVALID_ARG;
+    if (a->N < 0 || a->T < 0 || a->P < 0 || a->H < 1 || a->HV < 1 || a->HV % a->H != 0) return KDA_ERR_INVALID_ARG;
+    if (a->Dk < 1 || a->Dv < 1 || a->max_seqlen < 0 || a->T > 0x7FFFFFFF - 4096) return KDA_ERR_INVALID_ARG;
+    if (a->dtype != KDA_DT_F32 && a->dtype != KDA_DT_BF16) return KDA_ERR_INVALID_ARG;
+    if (a->algo != KDA_ALGO_AUTO && a->algo != KDA_ALGO_SIMT && a->algo != KDA_ALGO_TC) return KDA_ERR_INVALID_ARG;
+    if (!(a->g_min < 0.f) || !(a->l2_eps >= 0.f)) return KDA_ERR_INVALID_ARG;
+    if (a->gate_in_kernel < 0 || a->gate_in_kernel > 2) return KDA_ERR_INVALID_ARG;
+    if (a->Dk > 128 || a->Dv > 128 || a->Dv % 4 != 0) return KDA_ERR_UNSUPPORTED;
+    if ((long long)a->N * a->HV > 0x7FFFFFFFll) return KDA_ERR_UNSUPPORTED;     // the grid
+    if (!a->cu_seqlens && a->N != a->T) return KDA_ERR_INVALID_ARG;
+    if (!a->slots && a->N > a->P) return KDA_ERR_INVALID_ARG;
+    if (a->N == 0 || a->T == 0) return KDA_OK;
+    if (!a->q || !a->k || !a->v || !a->g || !a->beta || !a->o) return KDA_ERR_INVALID_ARG;
+    if (a->P > 0 && !a->pool) return KDA_ERR_INVALID_ARG;
+    if (a->gate_in_kernel && !a->A_log) return KDA_ERR_INVALID_ARG;
+    const bool bf16 = a->dtype == KDA_DT_BF16;
+    const size_t es = bf16 ? 2 : 4, gk = a->g_per_head ? 1 : (size_t)a->Dk;
+    const size_t rq = (size_t)a->H * a->Dk, rv = (size_t)a->HV * a->Dv, rg = a->HV * gk, rb = a->HV;
+    if (a->ld_q < (long long)rq || a->ld_k < (long long)rq || a->ld_v < (long long)rv || a->ld_g < (long long)rg ||
+        a->ld_beta < (long long)rb || a->ld_o < (long long)rv)
+        return KDA_ERR_INVALID_ARG;
+    const void *acts[] = {a->q, a->k, a->v, a->g, a->beta, a->o};
+    for (const void *p : acts)
+        if (!aligned(p, es)) return KDA_ERR_ALIGNMENT;
+    const void *p4[] = {a->A_log, a->dt_bias, a->cu_seqlens, a->slots};
+    for (const void *p : p4)
+        if (p && !aligned(p, 4)) return KDA_ERR_ALIGNMENT;
+    if (!aligned(a->pool, 16)) return KDA_ERR_ALIGNMENT;
+
+    Range r_in[] = {range_of(a->q, span_bytes(a->T, a->ld_q, rq, es)),
+                    range_of(a->k, span_bytes(a->T, a->ld_k, rq, es)),
+                    range_of(a->v, span_bytes(a->T, a->ld_v, rv, es)),
+                    range_of(a->g, span_bytes(a->T, a->ld_g, rg, es)),
+                    range_of(a->beta, span_bytes(a->T, a->ld_beta, rb, es)),
+                    range_of(a->A_log, a->A_log ? (size_t)a->HV * 4 : 0),
+                    range_of(a->dt_bias, a->dt_bias ? a->HV * gk * 4 : 0),
+                    range_of(a->cu_seqlens, a->cu_seqlens ? ((size_t)a->N + 1) * 4 : 0),
+                    range_of(a->slots, a->slots ? (size_t)a->N * 4 : 0),
+                    range_of(a->fresh, a->fresh ? (size_t)a->N : 0)};
+    Range r_pool = range_of(a->pool, (size_t)a->P * a->HV * a->Dk * a->Dv * 4);
+    Range r_o = range_of(a->o, span_bytes(a->T, a->ld_o, rv, es));
+    for (Range r : r_in)
+        if (overlaps(r_o, r) || overlaps(r_pool, r)) return KDA_ERR_ALIAS;
+    if (overlaps(r_o, r_pool)) return KDA_ERR_ALIAS;
+
+    kda::PackedParams p;
+    p.N = a->N; p.T = a->T; p.P = a->P; p.H = a->H; p.HV = a->HV; p.Dk = a->Dk; p.Dv = a->Dv;
+    p.group = a->HV / a->H;
+    p.g_min = a->g_min; p.scale = a->scale; p.l2_eps = a->l2_eps;
+    p.l2norm = a->qk_l2norm_in_kernel != 0;
+    p.beta_sigmoid = a->beta_sigmoid_in_kernel != 0;
+    p.gate_in = a->gate_in_kernel;
+    p.g_per_head = a->g_per_head != 0;
+    p.ldq = a->ld_q; p.ldk = a->ld_k; p.ldv = a->ld_v; p.ldg = a->ld_g; p.ldb = a->ld_beta; p.ldo = a->ld_o;
+    p.q = a->q; p.k = a->k; p.v = a->v; p.g = a->g; p.beta = a->beta;
+    p.A_log = a->A_log; p.dt_bias = a->dt_bias;
+    p.cu = a->cu_seqlens; p.slots = a->slots; p.fresh = a->fresh;
+    p.pool = a->pool; p.o = a->o;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+
+    // What the lengths can be: one row each without bounds, else the caller's bound or all rows.
+    int max_len = a->cu_seqlens ? a->T : 1;
+    if (a->cu_seqlens && a->max_seqlen > 0 && a->max_seqlen < max_len) max_len = a->max_seqlen;
+    constexpr int kAll = 0x7FFFFFFF;
+    if (a->algo == KDA_ALGO_TC) {
+        if (!kda::packed_chunk_shape(p, bf16)) return KDA_ERR_UNSUPPORTED;
+        if (!kda::packed_chunk_aligned(p)) return KDA_ERR_ALIGNMENT;
+        p.split = 0;
+        return cuda_status(kda::launch_packed_chunk(p, s));
+    }
+    const bool chunk = a->algo == KDA_ALGO_AUTO && max_len > kda::kPackedSplit && kda::packed_chunk_shape(p, bf16) &&
+                       kda::packed_chunk_aligned(p);
+    p.split = chunk ? kda::kPackedSplit : kAll;
+    if (chunk) {
+        const kda_status st = cuda_status(kda::launch_packed_chunk(p, s));
+        if (st != KDA_OK) return st;
+    }
+    return cuda_status(kda::launch_packed_recurrent(p, bf16, max_len, s));
+}
+
+kda_status kda_packed_conv(const kda_packed_conv_args *a, void *stream) {
+    if (!a) return KDA_ERR_INVALID_ARG;
+    if (a->N < 0 || a->T < 0 || a->P < 0 || a->C < 1 || a->K < 1 || a->K > 4 || !(a->l2_eps >= 0.f))
+        return KDA_ERR_INVALID_ARG;
+    if (a->dtype != KDA_DT_F32 && a->dtype != KDA_DT_BF16) return KDA_ERR_INVALID_ARG;
+    if (a->T > 0x7FFFFFFF - 4096) return KDA_ERR_INVALID_ARG;
+    if (a->head_dim != 0 && a->head_dim != 128) return KDA_ERR_UNSUPPORTED;
+    if (a->C % 128 != 0) return KDA_ERR_UNSUPPORTED;
+    if (!a->cu_seqlens && a->N != a->T) return KDA_ERR_INVALID_ARG;
+    if (!a->slots && a->N > a->P && a->K > 1) return KDA_ERR_INVALID_ARG;
+    if (a->N == 0 || a->T == 0) return KDA_OK;
+    if (!a->x || !a->w || !a->y || (a->K > 1 && a->P > 0 && !a->pool)) return KDA_ERR_INVALID_ARG;
+    if (a->ld_x < a->C || a->ld_y < a->C) return KDA_ERR_INVALID_ARG;
+    const bool bf16 = a->dtype == KDA_DT_BF16;
+    const size_t es = bf16 ? 2 : 4;
+    const void *p16[] = {a->x, a->y, a->pool};
+    for (const void *p : p16)
+        if (p && !aligned(p, 16)) return KDA_ERR_ALIGNMENT;
+    if (a->ld_x * es % 16 != 0 || a->ld_y * es % 16 != 0) return KDA_ERR_ALIGNMENT;
+    const void *p4[] = {a->w, a->bias, a->cu_seqlens, a->slots};
+    for (const void *p : p4)
+        if (p && !aligned(p, 4)) return KDA_ERR_ALIGNMENT;
+    Range r_in[] = {range_of(a->x, span_bytes(a->T, a->ld_x, a->C, es)), range_of(a->w, (size_t)a->C * a->K * 4),
+                    range_of(a->bias, a->bias ? (size_t)a->C * 4 : 0),
+                    range_of(a->cu_seqlens, a->cu_seqlens ? ((size_t)a->N + 1) * 4 : 0),
+                    range_of(a->slots, a->slots ? (size_t)a->N * 4 : 0),
+                    range_of(a->fresh, a->fresh ? (size_t)a->N : 0)};
+    Range r_y = range_of(a->y, span_bytes(a->T, a->ld_y, a->C, es));
+    Range r_pool = range_of(a->pool, a->pool ? (size_t)a->P * (a->K - 1) * a->C * es : 0);
+    for (Range r : r_in)
+        if (overlaps(r_y, r) || overlaps(r_pool, r)) return KDA_ERR_ALIAS;
+    if (overlaps(r_y, r_pool)) return KDA_ERR_ALIAS;
+    kda::PackedConvParams p;
+    p.N = a->N; p.T = a->T; p.P = a->K > 1 || a->slots ? a->P : a->N;
+    p.C = a->C; p.K = a->K; p.head_dim = a->head_dim; p.silu = a->silu != 0;
+    p.l2_eps = a->l2_eps;
+    p.ldx = a->ld_x; p.ldy = a->ld_y;
+    p.x = a->x; p.w = a->w; p.bias = a->bias; p.cu = a->cu_seqlens; p.slots = a->slots; p.fresh = a->fresh;
+    p.pool = a->pool; p.y = a->y;
+    return cuda_status(kda::launch_packed_conv(p, bf16, static_cast<cudaStream_t>(stream)));
+}
+
+// The plan reads activations in vectors when every one of them starts on 16
+// bytes; rows and groups keep that alignment where their sizes allow it.
+static bool group_norm_sizes(int N, int L, int C, int G, int dtype) {
+    return N >= 0 && L >= 1 && C >= 1 && G >= 1 && C % G == 0 && (dtype == KDA_DT_F32 || dtype == KDA_DT_BF16);
+}
+
+unsigned long long kda_group_norm_workspace(int N, int L, int C, int G, int dtype, int backward) {
+    if (!group_norm_sizes(N, L, C, G, dtype) || N == 0) return 0;
+    const bool bf16 = dtype == KDA_DT_BF16;
+    // the larger of the plans with and without 16-byte aligned pointers
+    const size_t a = kda::group_norm_plan(N, L, C, G, bf16, backward != 0, true).ws_floats;
+    const size_t b = kda::group_norm_plan(N, L, C, G, bf16, backward != 0, false).ws_floats;
+    return (a > b ? a : b) * sizeof(float);
+}
+
+static kda_status group_norm(const kda_group_norm_args *a, void *stream, bool backward) {
+    if (!a) return KDA_ERR_INVALID_ARG;
+    if (!group_norm_sizes(a->N, a->L, a->C, a->G, a->dtype) || !(a->eps >= 0.f)) return KDA_ERR_INVALID_ARG;
+    if (a->act < KDA_ACT_NONE || a->act > KDA_ACT_SIGMOID) return KDA_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool bf16 = a->dtype == KDA_DT_BF16;
+    const size_t es = bf16 ? 2 : 4;
+    const size_t nx = (size_t)a->N * a->L * a->C * es, nc = (size_t)a->C * 4, ns = (size_t)a->N * a->G * 4;
+    // the grid's limit, and the element counts of a slab that the kernels keep in an int
+    if ((long long)a->N * a->L > 0x7FFFFFFFll || (long long)a->N * a->G > 0x7FFFFFFFll ||
+        (long long)a->L * (a->C / a->G) > 0x7FFFFFFFll)
+        return KDA_ERR_UNSUPPORTED;
+    if (backward && a->dgate && !a->gate) return KDA_ERR_INVALID_ARG;
+    const float *f4[] = {a->weight, a->bias, a->mean, a->rstd, a->dweight, a->dbias};
+    for (const float *p : f4)
+        if (p && !aligned(p, 4)) return KDA_ERR_ALIGNMENT;
+    if (a->N == 0) {
+        if (backward && a->dweight && cudaMemsetAsync(a->dweight, 0, nc, s) != cudaSuccess) return KDA_ERR_CUDA;
+        if (backward && a->dbias && cudaMemsetAsync(a->dbias, 0, nc, s) != cudaSuccess) return KDA_ERR_CUDA;
+        return KDA_OK;
+    }
+    if (!a->x || !a->mean || !a->rstd || (backward ? !a->dy : !a->y)) return KDA_ERR_INVALID_ARG;
+    const unsigned long long need = kda_group_norm_workspace(a->N, a->L, a->C, a->G, a->dtype, backward);
+    if (need && !a->workspace) return KDA_ERR_INVALID_ARG;
+    if (!aligned(a->workspace, 16)) return KDA_ERR_ALIGNMENT;
+    const void *acts[] = {a->x, a->gate, backward ? a->dy : a->y, backward ? a->dx : nullptr,
+                          backward ? a->dgate : nullptr};
+    bool vec = true;
+    for (const void *p : acts) {
+        if (!aligned(p, es)) return KDA_ERR_ALIGNMENT;
+        vec = vec && aligned(p, 16);
+    }
+    Range in[] = {range_of(a->x, nx), range_of(a->gate, a->gate ? nx : 0),
+                  range_of(a->weight, a->weight ? nc : 0), range_of(a->bias, a->bias ? nc : 0),
+                  range_of(a->dy, backward ? nx : 0), range_of(a->mean, backward ? ns : 0),
+                  range_of(a->rstd, backward ? ns : 0)};
+    Range out[] = {range_of(a->y, backward ? 0 : nx), range_of(a->mean, backward ? 0 : ns),
+                   range_of(a->rstd, backward ? 0 : ns), range_of(a->dx, backward && a->dx ? nx : 0),
+                   range_of(a->dgate, backward && a->dgate ? nx : 0),
+                   range_of(a->dweight, backward && a->dweight ? nc : 0),
+                   range_of(a->dbias, backward && a->dbias ? nc : 0),
+                   range_of(a->workspace, need)};
+    const int n_out = sizeof(out) / sizeof(out[0]);
+    for (int i = 0; i < n_out; ++i) {
+        for (Range r : in)
+            if (overlaps(out[i], r)) return KDA_ERR_ALIAS;
+        for (int j = i + 1; j < n_out; ++j)
+            if (overlaps(out[i], out[j])) return KDA_ERR_ALIAS;
+    }
+    kda::GroupNormParams p;
+    p.N = a->N; p.L = a->L; p.C = a->C; p.G = a->G; p.D = a->C / a->G;
+    p.act = a->act; p.eps = a->eps;
+    p.x = a->x; p.gate = a->gate; p.dy = a->dy; p.weight = a->weight; p.bias = a->bias;
+    p.y = a->y; p.dx = a->dx; p.dgate = a->dgate; p.mean = a->mean; p.rstd = a->rstd;
+    p.dweight = a->dweight; p.dbias = a->dbias; p.ws = static_cast<float *>(a->workspace);
+    const kda::GroupNormPlan pl = kda::group_norm_plan(a->N, a->L, a->C, a->G, bf16, backward, vec);
+    return cuda_status(backward ? kda::launch_group_norm_bwd(p, pl, bf16, s) : kda::launch_group_norm_fwd(p, pl, bf16, s));
+}
+
+kda_status kda_group_norm_fwd(const kda_group_norm_args *a, void *stream) { return group_norm(a, stream, false); }
+
+kda_status kda_group_norm_bwd(const kda_group_norm_args *a, void *stream) { return group_norm(a, stream, true); }
+
 kda_status kda_device_status(void *stream) {
-    unsigned int word = 0, step_word = 0, conv_word = 0;
+    unsigned int word = 0, more[5] = {};
     cudaError_t e = kda::read_and_clear_device_error(static_cast<cudaStream_t>(stream), &word);
-    if (e == cudaSuccess) e = kda::read_and_clear_step_error(&step_word);
-    if (e == cudaSuccess) e = kda::read_and_clear_conv_error(&conv_word);
+    if (e == cudaSuccess) e = kda::read_and_clear_step_error(&more[0]);
+    if (e == cudaSuccess) e = kda::read_and_clear_conv_error(&more[1]);
+    if (e == cudaSuccess) e = kda::read_and_clear_packed_error(&more[2]);
+    if (e == cudaSuccess) e = kda::read_and_clear_packed_chunk_error(&more[3]);
+    if (e == cudaSuccess) e = kda::read_and_clear_packed_conv_error(&more[4]);
     if (e != cudaSuccess) return KDA_ERR_CUDA;
-    word |= step_word | conv_word;
+    for (unsigned int w : more) word |= w;
     if (word & 1u) return KDA_ERR_TIMEOUT;
     return (word & 2u) ? KDA_ERR_RANGE : KDA_OK;
 }

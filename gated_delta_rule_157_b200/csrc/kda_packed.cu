@@ -1,0 +1,274 @@
+// kda_packed_fwd, recurrent form: every (sequence, value head) token by token
+// in fp32, state in registers from its load to its store.
+//
+// With ka = k (.) a, qa = q (.) a (a the decay of the token), both inner
+// products read the state as it was before the token,
+//
+//     e = v - S^T ka,    o = S^T qa + (q . k) beta e,    S <- a (.) S + k (beta e)^T,
+//
+// so one pass over the registers and one reduction serve both.  State columns
+// are independent: a warp owns CW = 4 * 32 / RG columns of all Dk rows, lane =
+// (row group, quad of columns); only the RG row groups meet, in log2(RG)
+// shuffle steps, and no warp waits for another inside a tile of tokens.  What
+// depends on the token alone (norms, gates, ka, qa) is prepared by the block
+// for a tile of two tokens per warp into a double shared buffer while the
+// previous tile is computed: one block barrier per tile.
+#include "kda_packed.cuh"
+
+namespace kda {
+namespace {
+
+__device__ unsigned int g_packed_error = 0;
+
+constexpr int kRG = 8;                     // row groups (lanes along a column)
+constexpr int kCW = 4 * 32 / kRG;          // state columns per warp
+constexpr int kTPW = 2;                    // tokens a warp prepares per tile
+
+extern __shared__ float smem[];
+
+// Floats of one prepared token: ka, qa, k, a (one decay per channel) or k, q
+// (one per head), the row of v, and {beta, q . k, a}.
+__host__ __device__ constexpr int token_floats(int dkp, bool per_head) { return (per_head ? 2 : 4) * dkp + 128 + 4; }
+
+template <typename Tin, int RPL, bool PER_HEAD>
+struct TokenPrep {
+    static constexpr int DKP = RPL * kRG;
+    static constexpr int NC = (DKP + 31) / 32;
+    float q[NC], k[NC], g[NC], v[4], beta;
+
+    __device__ __forceinline__ void load(const PackedParams &p, long long row, int h, int hv, int lane) {
+        const Tin *qr = static_cast<const Tin *>(p.q) + row * p.ldq + (long long)h * p.Dk;
+        const Tin *kr = static_cast<const Tin *>(p.k) + row * p.ldk + (long long)h * p.Dk;
+        const Tin *vr = static_cast<const Tin *>(p.v) + row * p.ldv + (long long)hv * p.Dv;
+        const Tin *gr = static_cast<const Tin *>(p.g) + row * p.ldg + (long long)hv * (PER_HEAD ? 1 : p.Dk);
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int c = lane + 32 * i;
+            const bool in = c < p.Dk;
+            q[i] = in ? ld_act(qr, c) : 0.f;
+            k[i] = in ? ld_act(kr, c) : 0.f;
+            if (!PER_HEAD) g[i] = in ? ld_act(gr, c) : 0.f;
+        }
+        if (PER_HEAD) g[0] = ld_act(gr, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = lane + 32 * i < p.Dv ? ld_act(vr, lane + 32 * i) : 0.f;
+        beta = ld_act(static_cast<const Tin *>(p.beta) + row * p.ldb, hv);
+    }
+
+    __device__ __forceinline__ void store(const PackedParams &p, int hv, float ea, int lane, float *out) {
+        float sq = 0.f, sk = 0.f, qk = 0.f;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            sq = fmaf(q[i], q[i], sq);
+            sk = fmaf(k[i], k[i], sk);
+            qk = fmaf(q[i], k[i], qk);
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+            sq += __shfl_xor_sync(0xffffffffu, sq, off);
+            sk += __shfl_xor_sync(0xffffffffu, sk, off);
+            qk += __shfl_xor_sync(0xffffffffu, qk, off);
+        }
+        const float rq = p.l2norm ? p.scale / sqrtf(sq + p.l2_eps) : p.scale;
+        const float rk = p.l2norm ? 1.f / sqrtf(sk + p.l2_eps) : 1.f;
+        float a_head = 0.f;
+        if (PER_HEAD) {
+            const float b = p.dt_bias && p.gate_in ? p.dt_bias[hv] : 0.f;
+            a_head = expf(p.gate_in ? kda_gate(p.gate_in, g[0], b, ea, p.g_min) : g[0]);
+        }
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int c = lane + 32 * i;
+            if (c >= DKP) break;
+            const float kn = k[i] * rk, qn = q[i] * rq;
+            if (PER_HEAD) {
+                out[c] = kn;
+                out[DKP + c] = qn;
+            } else {
+                const bool in = c < p.Dk;
+                const float b = in && p.dt_bias && p.gate_in ? p.dt_bias[(size_t)hv * p.Dk + c] : 0.f;
+                const float a = in ? expf(p.gate_in ? kda_gate(p.gate_in, g[i], b, ea, p.g_min) : g[i]) : 0.f;
+                out[c] = kn * a;
+                out[DKP + c] = qn * a;
+                out[2 * DKP + c] = kn;
+                out[3 * DKP + c] = a;
+            }
+        }
+        float *vo = out + (PER_HEAD ? 2 : 4) * DKP;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) vo[lane + 32 * i] = v[i];
+        if (lane == 0) {
+            vo[128] = p.beta_sigmoid ? sigmoidf_(beta) : beta;
+            vo[129] = qk * rq * rk;
+            vo[130] = a_head;
+        }
+    }
+};
+
+template <typename Tin, int RPL, bool PER_HEAD>
+__global__ void __launch_bounds__(256)
+packed_recurrent_kernel(const PackedParams p) {
+    constexpr int DKP = RPL * kRG;
+    constexpr int TF = token_floats(DKP, PER_HEAD);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+    const int s = blockIdx.x / p.HV, hv = blockIdx.x % p.HV, h = hv / p.group;
+    const int rg = lane / (32 / kRG), quad = lane % (32 / kRG);
+    const int col = (blockIdx.y * warps + warp) * kCW + 4 * quad;
+    const bool col_ok = col < p.Dv;
+
+    const PackedSeq sq = packed_seq(p.cu, p.slots, p.T, p.P, s);
+    const bool repeat = __syncthreads_or(packed_repeat(p.slots, s, sq.slot, tid, blockDim.x));
+    if ((sq.bad || repeat) && tid == 0 && hv == 0 && blockIdx.y == 0) atomicOr(&g_packed_error, kPackedRange);
+    // a sequence without rows changes nothing
+    if (sq.bad || repeat || sq.slot < 0 || sq.len == 0 || sq.len > p.split) return;
+
+    // The state: rows (i / 4) * 4 RG + 4 rg + i % 4 of this lane's four columns,
+    // kept as row pairs so that the prepared vectors feed packed FMAs directly.
+    float *S = p.pool + ((size_t)sq.slot * p.HV + hv) * p.Dk * p.Dv + col;
+    float2 st[RPL / 2][4];
+    const bool zero = p.fresh && p.fresh[s];
+#pragma unroll
+    for (int i = 0; i < RPL; ++i) {
+        const int r = (i >> 2) * (4 * kRG) + 4 * rg + (i & 3);
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (!zero && col_ok && r < p.Dk) x = __ldcs(reinterpret_cast<const float4 *>(S + (size_t)r * p.Dv));
+        if ((i & 1) == 0) {
+            st[i >> 1][0].x = x.x; st[i >> 1][1].x = x.y; st[i >> 1][2].x = x.z; st[i >> 1][3].x = x.w;
+        } else {
+            st[i >> 1][0].y = x.x; st[i >> 1][1].y = x.y; st[i >> 1][2].y = x.z; st[i >> 1][3].y = x.w;
+        }
+    }
+
+    const float ea = p.gate_in ? expf(p.A_log[hv]) : 0.f;
+    const int tile = kTPW * warps;
+    TokenPrep<Tin, RPL, PER_HEAD> raw[kTPW];
+#pragma unroll
+    for (int u = 0; u < kTPW; ++u) {
+        const int t = warp * kTPW + u;
+        if (t < sq.len) raw[u].load(p, (long long)sq.begin + t, h, hv, lane);
+    }
+    for (int t0 = 0, buf = 0; t0 < sq.len; t0 += tile, buf ^= 1) {
+        float *tok = smem + buf * tile * TF;
+#pragma unroll
+        for (int u = 0; u < kTPW; ++u) {
+            const int t = t0 + warp * kTPW + u;
+            if (t < sq.len) raw[u].store(p, hv, ea, lane, tok + (warp * kTPW + u) * TF);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < kTPW; ++u) {               // the next tile's rows, in flight meanwhile
+            const int t = t0 + tile + warp * kTPW + u;
+            if (t < sq.len) raw[u].load(p, (long long)sq.begin + t, h, hv, lane);
+        }
+        const int n = min(tile, sq.len - t0);
+#pragma unroll 1
+        for (int t = 0; t < n; ++t) {
+            const float *x = tok + t * TF;
+            const float *xk = x + 4 * rg, *xq = x + DKP + 4 * rg;      // ka, qa (or k, q)
+            float2 ak[4], aq[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) ak[c] = aq[c] = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < RPL / 4; ++i) {
+                const float4 k4 = *reinterpret_cast<const float4 *>(xk + i * 4 * kRG);
+                const float4 q4 = *reinterpret_cast<const float4 *>(xq + i * 4 * kRG);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    ak[c] = __ffma2_rn(make_float2(k4.x, k4.y), st[2 * i][c], ak[c]);
+                    aq[c] = __ffma2_rn(make_float2(q4.x, q4.y), st[2 * i][c], aq[c]);
+                    ak[c] = __ffma2_rn(make_float2(k4.z, k4.w), st[2 * i + 1][c], ak[c]);
+                    aq[c] = __ffma2_rn(make_float2(q4.z, q4.w), st[2 * i + 1][c], aq[c]);
+                }
+            }
+            float ks[4], qs[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                ks[c] = ak[c].x + ak[c].y;
+                qs[c] = aq[c].x + aq[c].y;
+            }
+#pragma unroll
+            for (int off = 32 / kRG; off < 32; off <<= 1) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    ks[c] += __shfl_xor_sync(0xffffffffu, ks[c], off);
+                    qs[c] += __shfl_xor_sync(0xffffffffu, qs[c], off);
+                }
+            }
+            const float *xv = x + (PER_HEAD ? 2 : 4) * DKP;
+            const float beta = xv[128], qk = xv[129], ah = xv[130];
+            float u[4], ov = 0.f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const float e = xv[(col & 127) + c] - (PER_HEAD ? ah * ks[c] : ks[c]);
+                u[c] = beta * e;
+                const float oc = fmaf(qk, u[c], PER_HEAD ? ah * qs[c] : qs[c]);
+                ov = rg == c ? oc : ov;
+            }
+            // row group c writes column c of the quad
+            if (rg < 4 && col_ok)
+                st_act(static_cast<Tin *>(p.o) + ((long long)sq.begin + t0 + t) * p.ldo + (long long)hv * p.Dv,
+                       (size_t)(col + rg), ov);
+#pragma unroll
+            for (int i = 0; i < RPL / 4; ++i) {
+                const float4 k4 = *reinterpret_cast<const float4 *>((PER_HEAD ? xk : xk + 2 * DKP) + i * 4 * kRG);
+                float4 a4 = make_float4(ah, ah, ah, ah);
+                if (!PER_HEAD) a4 = *reinterpret_cast<const float4 *>(xk + 3 * DKP + i * 4 * kRG);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const float2 uc = make_float2(u[c], u[c]);
+                    st[2 * i][c] = __ffma2_rn(make_float2(k4.x, k4.y), uc,
+                                              __fmul2_rn(make_float2(a4.x, a4.y), st[2 * i][c]));
+                    st[2 * i + 1][c] = __ffma2_rn(make_float2(k4.z, k4.w), uc,
+                                                  __fmul2_rn(make_float2(a4.z, a4.w), st[2 * i + 1][c]));
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < RPL; ++i) {
+        const int r = (i >> 2) * (4 * kRG) + 4 * rg + (i & 3);
+        float4 x;
+        if ((i & 1) == 0)
+            x = make_float4(st[i >> 1][0].x, st[i >> 1][1].x, st[i >> 1][2].x, st[i >> 1][3].x);
+        else
+            x = make_float4(st[i >> 1][0].y, st[i >> 1][1].y, st[i >> 1][2].y, st[i >> 1][3].y);
+        if (col_ok && r < p.Dk) __stcs(reinterpret_cast<float4 *>(S + (size_t)r * p.Dv), x);
+    }
+}
+
+template <typename Tin, int RPL, bool PER_HEAD>
+cudaError_t launch_one(const PackedParams &p, int warps, cudaStream_t s) {
+    const int all = (p.Dv + kCW - 1) / kCW;
+    const dim3 grid((unsigned)p.N * (unsigned)p.HV, (unsigned)((all + warps - 1) / warps));
+    const size_t bytes = (size_t)2 * kTPW * warps * token_floats(RPL * kRG, PER_HEAD) * sizeof(float);
+    auto kernel = packed_recurrent_kernel<Tin, RPL, PER_HEAD>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, 32 * warps, bytes, s>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename Tin>
+cudaError_t launch_type(const PackedParams &p, int warps, cudaStream_t s) {
+    if (p.Dk <= 64)
+        return p.g_per_head ? launch_one<Tin, 8, true>(p, warps, s) : launch_one<Tin, 8, false>(p, warps, s);
+    return p.g_per_head ? launch_one<Tin, 16, true>(p, warps, s) : launch_one<Tin, 16, false>(p, warps, s);
+}
+
+}  // namespace
+
+cudaError_t launch_packed_recurrent(const PackedParams &p, bool bf16, int max_len, cudaStream_t s) {
+    (void)max_len;
+    const int all = (p.Dv + kCW - 1) / kCW;
+    const int warps = all < 4 ? all : 4;
+    return bf16 ? launch_type<__nv_bfloat16>(p, warps, s) : launch_type<float>(p, warps, s);
+}
+
+cudaError_t read_and_clear_packed_error(unsigned int *out) {
+    cudaError_t e = cudaMemcpyFromSymbol(out, g_packed_error, sizeof(unsigned int));
+    if (e != cudaSuccess) return e;
+    unsigned int zero = 0;
+    return cudaMemcpyToSymbol(g_packed_error, &zero, sizeof(unsigned int));
+}
+
+}  // namespace kda

@@ -59,7 +59,8 @@ typedef enum {
     KDA_ERR_CUDA = 5,          /* a CUDA runtime call or launch failed */
     KDA_ERR_TIMEOUT = 6,       /* a bounded device-side wait gave up (see kda_device_status) */
     KDA_ERR_RANGE = 7          /* a log-decay given directly to the tensor-core kernel was
-                                  below g_min and was clamped (see kda_device_status) */
+                                  below g_min and was clamped, or a packed call skipped a
+                                  sequence for its bounds or slot (see kda_device_status) */
 } kda_status;
 
 typedef enum {
@@ -307,12 +308,146 @@ typedef struct {
  * overlap o or gate.  Errors as for kda_chunk_fwd. */
 kda_status kda_output_gate(const kda_gate_args *args, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Packed batches: sequences of different lengths laid one after another in
+ * T rows, their states in a pool of slots (serving: prefill, decode and
+ * verification of many requests at once).
+ *
+ *   cu_seqlens [N + 1] int32: sequence s is rows cu_seqlens[s] .. cu_seqlens[s+1]-1,
+ *              nondecreasing, within [0, T]; rows outside every sequence are
+ *              neither read nor written.  NULL: N == T sequences of one row each
+ *              (a decode step).
+ *   slots      [N] int32: the pool slot of each sequence; a negative slot skips
+ *              the sequence (a padded row of a captured batch): its output rows
+ *              stay as they were.  NULL: sequence s has slot s (needs N <= P).
+ *   fresh      [N] uint8: nonzero starts the sequence from a zero state (or
+ *              window) whatever its slot holds; NULL: none.
+ *
+ * These arrays live on the device and are read by the kernels, so a captured
+ * call replays with whatever they then hold.  A sequence of no rows changes
+ * nothing, its slot included.  A sequence whose bounds lie outside [0, T], whose
+ * slot is >= P, or whose slot an earlier sequence of the call also names, is
+ * skipped like a negative slot and reported by kda_device_status as
+ * KDA_ERR_RANGE.  Output rows that two sequences share (overlapping bounds)
+ * hold one of the two results.
+ * ------------------------------------------------------------------------- */
+
+/* The delta rule of kda_chunk_fwd / kda_step over a packed batch, each state
+ * read from and written back to its slot in place.  Activations may be strided
+ * views (columns of one fused projection): row r of x begins ld_x elements
+ * after row r - 1; heads and channels are contiguous inside a row.
+ *
+ * algo: KDA_ALGO_SIMT runs the recurrence token by token in fp32 (any width,
+ * dtype and decay); KDA_ALGO_TC the chunk form on the tensor cores (bf16,
+ * Dk = Dv = 128, g_per_head, any decay, 16-byte aligned rows; every product of
+ * rounded operands carries three bf16 terms of each, so the state keeps fp32
+ * accuracy), KDA_ERR_UNSUPPORTED or KDA_ERR_ALIGNMENT otherwise.
+ * KDA_ALGO_AUTO takes the chunk form for sequences longer than
+ * 32 rows where it applies and the recurrence for all others; both kernels
+ * then run, each on its sequences. */
+typedef struct {
+    int N;                     /* sequences */
+    int T;                     /* rows of q, k, v, g, beta and o, < 2^31 - 4096 */
+    int P;                     /* slots in the pool */
+    int H, HV, Dk, Dv;         /* as kda_step: Dk <= 128, Dv <= 128, Dv % 4 == 0 */
+    int max_seqlen;            /* upper bound of the lengths if the caller knows one, else 0;
+                                  picks kernels only: results do not depend on it */
+    int dtype;                 /* kda_dtype of q, k, v, g, beta and o */
+    int algo;                  /* kda_algo */
+    float g_min, scale, l2_eps;
+    int qk_l2norm_in_kernel, beta_sigmoid_in_kernel, gate_in_kernel;   /* as kda_chunk_fwd */
+    int g_per_head;
+    long long ld_q, ld_k, ld_v, ld_g, ld_beta, ld_o;   /* elements between rows, >= the row's own */
+    const void *q, *k;         /* [T, H, Dk]  */
+    const void *v;             /* [T, HV, Dv] */
+    const void *g;             /* [T, HV, Dk] ([T, HV] with g_per_head) */
+    const void *beta;          /* [T, HV] */
+    const float *A_log, *dt_bias;
+    const int *cu_seqlens, *slots;
+    const unsigned char *fresh;
+    float *pool;               /* [P, HV, Dk, Dv] fp32, 16-byte aligned */
+    void *o;                   /* [T, HV, Dv] */
+} kda_packed_args;
+
+/* Runs the above.  o must not overlap an input or the pool, nor the pool an
+ * input.  Errors as for kda_chunk_fwd. */
+kda_status kda_packed_fwd(const kda_packed_args *args, void *stream);
+
+/* kda_short_conv over a packed batch: the K - 1 rows before a sequence's first
+ * come from its slot of the pool (or are zero if fresh), and the slot receives
+ * the last K - 1 rows of the old window followed by the sequence. */
+typedef struct {
+    int N, T, P;               /* sequences, rows, slots */
+    int C;                     /* channels, C % 128 == 0 */
+    int K;                     /* taps, 1..4 */
+    int head_dim;              /* 0 or 128: L2-normalise every 128 channels */
+    int silu;
+    int dtype;                 /* kda_dtype of x, y and pool */
+    float l2_eps;
+    long long ld_x, ld_y;      /* elements between rows */
+    const void *x;             /* [T, C] */
+    const float *w;            /* [C, K] fp32 */
+    const float *bias;         /* [C] fp32, or NULL */
+    const int *cu_seqlens, *slots;
+    const unsigned char *fresh;
+    void *pool;                /* [P, K-1, C], updated in place (not read when K == 1) */
+    void *y;                   /* [T, C] */
+} kda_packed_conv_args;
+
+/* Runs the above.  x, y, pool and their rows must be 16-byte aligned; y must
+ * not overlap an input or the pool, nor the pool an input. */
+kda_status kda_packed_conv(const kda_packed_conv_args *args, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Group norm with an activation over channels-last rows, forward and backward
+ * (the epilogue of gated linear attention layers beside kda_output_gate; with
+ * L = 1 every token's heads are normalised on their own):
+ *
+ *     h = (x - mean) / sqrt(var + eps)      over the L rows and C / G channels of (n, group)
+ *     u = weight * h + bias
+ *     y = f(u),  or u * f(gate) when gate is given;   f: identity, SiLU or sigmoid
+ * ------------------------------------------------------------------------- */
+typedef enum {
+    KDA_ACT_NONE = 0,
+    KDA_ACT_SILU = 1,
+    KDA_ACT_SIGMOID = 2
+} kda_act;
+
+typedef struct {
+    int N, L, C, G;            /* x [N, L, C]; G groups of C / G channels; L >= 1 */
+    int act;                   /* kda_act */
+    int dtype;                 /* kda_dtype of x, gate, y, dy, dx and dgate */
+    float eps;                 /* >= 0 */
+    const void *x;
+    const void *gate;          /* [N, L, C], or NULL */
+    const float *weight, *bias;/* [C] fp32, or NULL (1 and 0) */
+    void *y;                   /* forward: [N, L, C] output */
+    float *mean, *rstd;        /* [N, G] fp32: forward outputs, backward inputs */
+    const void *dy;            /* backward: [N, L, C] */
+    void *dx, *dgate;          /* backward outputs, or NULL; dgate needs gate */
+    float *dweight, *dbias;    /* backward outputs [C] fp32, or NULL */
+    void *workspace;           /* kda_group_norm_workspace bytes, 16-byte aligned, not shared by
+                                  calls that may run at the same time */
+} kda_group_norm_args;
+
+/* Bytes of workspace the forward (backward = 0) or the backward of these sizes
+ * needs (0: none, workspace may be NULL); 0 for invalid sizes. */
+unsigned long long kda_group_norm_workspace(int N, int L, int C, int G, int dtype, int backward);
+
+/* Forward: writes y, mean and rstd.  Backward: writes dx and dgate in x's type,
+ * dweight and dbias in fp32, summed in a fixed order (the same bits every run).
+ * Any C, G with C % G == 0; activation pointers aligned to their elements
+ * (16-byte aligned ones are read in vectors).  No output may overlap an input,
+ * another output or the workspace.  N == 0 writes zeros to dweight and dbias. */
+kda_status kda_group_norm_fwd(const kda_group_norm_args *args, void *stream);
+kda_status kda_group_norm_bwd(const kda_group_norm_args *args, void *stream);
+
 /* Reads and clears the device error words of the current device (chunk
- * kernel, decode step, layer prologue) after synchronising `stream`.
- * Returns KDA_OK, KDA_ERR_TIMEOUT (a bounded wait gave up since the last
- * call; takes precedence), KDA_ERR_RANGE (a
- * tensor-core call clamped a caller-given log-decay below g_min) or
- * KDA_ERR_CUDA. */
+ * kernel, decode step, layer prologue, packed kernels) after synchronising
+ * `stream`.  Returns KDA_OK, KDA_ERR_TIMEOUT (a bounded wait gave up since the
+ * last call; takes precedence), KDA_ERR_RANGE (a
+ * tensor-core call clamped a caller-given log-decay below g_min, or a packed
+ * call skipped a sequence for its bounds or its slot) or KDA_ERR_CUDA. */
 kda_status kda_device_status(void *stream);
 
 /* Test hook for the failure path of the tensor-core chunk kernel (no

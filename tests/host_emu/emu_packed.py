@@ -1,0 +1,170 @@
+"""Host emulation of the packed kernels and of group norm -- TEST INFRASTRUCTURE.
+
+Compiles kda_packed.cu, kda_packed_conv.cu and kda_group_norm.cu (cut before
+their launchers, as emu_build does for the other kernels) with g++ and
+AddressSanitizer or ThreadSanitizer.  The library never uses any of this.
+"""
+import os
+import re
+
+import emu_build
+from emu_build import CSRC, HERE, OUT, _POISON, SMEM_FLOATS
+
+LIB = os.path.join(OUT, "libkda_packed_emu.so")
+
+# What the packed kernels use beyond the stand-in headers.
+_MORE = r'''
+inline int __any_sync(unsigned m, int pred) {
+    float r = pred ? 1.f : 0.f;
+    for (int off = 16; off > 0; off >>= 1) r += __shfl_xor_sync(m, r, off);
+    return r != 0.f;
+}
+using std::memcpy;
+'''
+
+_RUN_RECURRENT = _POISON + r'''
+extern "C" int emu_sizeof_packed_params(void) { return (int)sizeof(kda::PackedParams); }
+template <typename Tin, int RPL, bool PER_HEAD>
+static void run_one(const kda::PackedParams &p, int warps) {
+    using namespace kda;
+    const int all = (p.Dv + kCW - 1) / kCW;
+    emu_poison((size_t)2 * kTPW * warps * token_floats(RPL * kRG, PER_HEAD) * sizeof(float));
+    emu_launch(dim3(p.N * p.HV, (all + warps - 1) / warps), dim3(32 * warps),
+               [&] { packed_recurrent_kernel<Tin, RPL, PER_HEAD>(p); });
+}
+template <typename Tin>
+static void run_type(const kda::PackedParams &p, int warps) {
+    if (p.Dk <= 64) p.g_per_head ? run_one<Tin, 8, true>(p, warps) : run_one<Tin, 8, false>(p, warps);
+    else p.g_per_head ? run_one<Tin, 16, true>(p, warps) : run_one<Tin, 16, false>(p, warps);
+}
+extern "C" int emu_packed_recurrent(kda::PackedParams *p, int bf16, int warps) {
+    kda::g_packed_error = 0;
+    if (bf16) run_type<__nv_bfloat16>(*p, warps);
+    else run_type<float>(*p, warps);
+    return (int)kda::g_packed_error;
+}
+'''
+_RUN_CONV = _POISON + r'''
+extern "C" int emu_sizeof_packed_conv_params(void) { return (int)sizeof(kda::PackedConvParams); }
+template <typename Tin>
+static void run_conv(const kda::PackedConvParams &p, int run) {
+    using namespace kda;
+    emu_poison(0);
+    const long long warps = ((long long)p.T + run - 1) / run * ((p.C + 255) / 256);
+    const dim3 grid((unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32)));
+    switch (p.K) {
+        case 1: emu_launch(grid, dim3(kThreads), [&] { packed_conv_kernel<Tin, 1>(p, run); }); break;
+        case 2: emu_launch(grid, dim3(kThreads), [&] { packed_conv_kernel<Tin, 2>(p, run); }); break;
+        case 3: emu_launch(grid, dim3(kThreads), [&] { packed_conv_kernel<Tin, 3>(p, run); }); break;
+        default: emu_launch(grid, dim3(kThreads), [&] { packed_conv_kernel<Tin, 4>(p, run); }); break;
+    }
+}
+extern "C" int emu_packed_conv(kda::PackedConvParams *p, int bf16, int run) {
+    kda::g_packed_conv_error = 0;
+    if (bf16) run_conv<__nv_bfloat16>(*p, run);
+    else run_conv<float>(*p, run);
+    return (int)kda::g_packed_conv_error;
+}
+'''
+_RUN_NORM = _POISON + r'''
+extern "C" int emu_sizeof_group_norm_params(void) { return (int)sizeof(kda::GroupNormParams); }
+extern "C" long long emu_group_norm_ws(int N, int L, int C, int G, int bf16, int backward, int aligned) {
+    return (long long)kda::group_norm_plan(N, L, C, G, bf16, backward, aligned).ws_floats;
+}
+template <typename Tin, int VEC, int VPT, bool GATED>
+static void run_held(const kda::GroupNormParams &p, const kda::GroupNormPlan &pl, bool backward) {
+    using namespace kda;
+    emu_poison(kHeldSmem);
+    const dim3 grid(pl.gx, pl.gy);
+    if (!backward) {
+        emu_launch(grid, dim3(kThreads), [&] { gn_held_fwd_kernel<Tin, VEC, VPT, GATED>(p, pl); });
+        return;
+    }
+    if constexpr (VPT <= 2) {
+        emu_launch(grid, dim3(kThreads), [&] { gn_held_bwd_kernel<Tin, VEC, VPT, GATED>(p, pl); });
+        emu_poison(kTileSmem);
+        emu_launch(dim3((p.C + 31) / 32), dim3(kThreads), [&] { gn_sum_kernel(p.ws, pl.gy, p.C, p.dweight, p.dbias); });
+    }
+}
+template <typename Tin, int VEC, bool GATED>
+static void run_tiled(const kda::GroupNormParams &p, const kda::GroupNormPlan &pl, bool backward) {
+    using namespace kda;
+    emu_poison(kTileSmem);
+    const dim3 grid(pl.gx, pl.gy);
+    if (!backward) {
+        emu_launch(grid, dim3(kThreads), [&] { gn_tile_stats_kernel<Tin, VEC>(p, pl); });
+        emu_launch(dim3(p.N * p.G), dim3(kThreads), [&] { gn_tile_mean_kernel(p, pl); });
+        emu_launch(grid, dim3(kThreads), [&] { gn_tile_fwd_kernel<Tin, VEC, GATED>(p, pl); });
+        return;
+    }
+    float *gsum = p.ws + (size_t)p.N * pl.tiles * 2 * p.C;
+    emu_launch(grid, dim3(kThreads), [&] { gn_tile_dsum_kernel<Tin, VEC, GATED>(p, pl); });
+    emu_launch(dim3(p.N * p.G), dim3(kThreads), [&] { gn_tile_gsum_kernel(p, pl, gsum); });
+    emu_launch(dim3((p.C + 31) / 32), dim3(kThreads),
+               [&] { gn_sum_kernel(p.ws, p.N * pl.tiles, p.C, p.dweight, p.dbias); });
+    emu_launch(grid, dim3(kThreads), [&] { gn_tile_bwd_kernel<Tin, VEC, GATED>(p, pl, gsum); });
+}
+template <typename Tin, int VEC, bool GATED>
+static void run_norm(const kda::GroupNormParams &p, const kda::GroupNormPlan &pl, bool backward) {
+    if (!pl.held) run_tiled<Tin, VEC, GATED>(p, pl, backward);
+    else if (pl.vpt == 1) run_held<Tin, VEC, 1, GATED>(p, pl, backward);
+    else if (pl.vpt == 2) run_held<Tin, VEC, 2, GATED>(p, pl, backward);
+    else run_held<Tin, VEC, 4, GATED>(p, pl, backward);
+}
+template <typename Tin, int FULL>
+static void run_norm_type(const kda::GroupNormParams &p, const kda::GroupNormPlan &pl, bool backward) {
+    if (pl.vec == FULL) p.gate ? run_norm<Tin, FULL, true>(p, pl, backward) : run_norm<Tin, FULL, false>(p, pl, backward);
+    else p.gate ? run_norm<Tin, 1, true>(p, pl, backward) : run_norm<Tin, 1, false>(p, pl, backward);
+}
+extern "C" int emu_group_norm(kda::GroupNormParams *p, int bf16, int backward, int aligned) {
+    kda::GroupNormPlan pl = kda::group_norm_plan(p->N, p->L, p->C, p->G, bf16, backward, aligned);
+    if (pl.held && pl.gy > 2) pl.gy = 2;      // few blocks, so that each walks several rows
+    if (bf16) run_norm_type<__nv_bfloat16, 8>(*p, pl, backward);
+    else run_norm_type<float, 4>(*p, pl, backward);
+    return pl.held;
+}
+'''
+
+
+def _unit(src_name, runner, extra=None):
+    """As emu_build._unit; `extra` = (from, to): a stretch of the source behind
+    the cut (host functions that the runner needs), kept too."""
+    s = open(os.path.join(CSRC, src_name)).read()
+    m = re.search(r"^(template <[^>]*>\n(static )?)?cudaError_t launch_", s, re.M)
+    body = s[: m.start()]
+    if "\n}  // namespace\n" not in body:
+        body += "\n}  // namespace\n"
+    if extra:
+        a = s.index(extra[0])
+        body += "namespace {\n" + s[a: s.index(extra[1])] if extra[2] else s[a: s.index(extra[1])]
+    body += "}  // namespace kda\n"
+    body = body.replace("extern __shared__", "extern").replace("__shared__", "static")
+    head = ('#include <functional>\n#include "cuda_runtime.h"\n' + _MORE +
+            "void emu_launch(dim3 grid, dim3 block, const std::function<void()> &fn);\n"
+            "namespace kda { namespace { alignas(16) float smem[%d]; } }\n" % SMEM_FLOATS)
+    return head + "#line 1 \"%s\"\n" % src_name + body + runner
+
+
+def _deps():
+    return [os.path.join(CSRC, f) for f in ("kda_packed.cu", "kda_packed_conv.cu", "kda_group_norm.cu",
+                                            "kda_packed.cuh", "kda_group_norm.cuh", "kda_internal.cuh")] + \
+        [os.path.join(HERE, f) for f in ("emu_packed.py", "emu_build.py", "emu_rt.cpp", "fakeinc/cuda_runtime.h",
+                                         "fakeinc/cuda_bf16.h")]
+
+
+def build(force=False, sanitizer="address"):
+    lib = LIB if sanitizer == "address" else LIB[:-3] + "_tsan.so"
+    if not force and os.path.exists(lib) and all(os.path.getmtime(d) <= os.path.getmtime(lib) for d in _deps()):
+        return lib
+    units = {"emu_packed.cpp": _unit("kda_packed.cu", _RUN_RECURRENT),
+             "emu_packed_conv.cpp": _unit("kda_packed_conv.cu", _RUN_CONV),
+             "emu_group_norm.cpp": _unit("kda_group_norm.cu", _RUN_NORM,
+                                         ("int pow2_at_least", "cudaError_t launch_group_norm_fwd", True))}
+    if sanitizer != "address":
+        units = {n: t.replace("#include <sanitizer/asan_interface.h>", "#define ASAN_POISON_MEMORY_REGION(a, b)\n"
+                              "#define ASAN_UNPOISON_MEMORY_REGION(a, b)") for n, t in units.items()}
+    return emu_build.compile_units(units, lib, sanitizer)
+
+
+if __name__ == "__main__":
+    print(build(force=True))
