@@ -1,8 +1,9 @@
 """Host emulation of the packed kernels and of group norm -- TEST INFRASTRUCTURE.
 
-Compiles kda_packed.cu, kda_packed_conv.cu and kda_group_norm.cu (cut before
-their launchers, as emu_build does for the other kernels) with g++ and
-AddressSanitizer or ThreadSanitizer.  The library never uses any of this.
+Compiles kda_packed.cu, kda_packed_conv.cu, kda_group_norm.cu and
+kda_packed_tc.cu (cut before their launchers, as emu_build does for the other
+kernels; the last over tcinc/tc_ptx.cuh, the host model of the tcgen05, TMA and
+mbarrier instructions) with g++ and AddressSanitizer or ThreadSanitizer.  The library never uses any of this.
 """
 import os
 import re
@@ -19,6 +20,21 @@ inline int __any_sync(unsigned m, int pred) {
     for (int off = 16; off > 0; off >>= 1) r += __shfl_xor_sync(m, r, off);
     return r != 0.f;
 }
+// Any other lane's value, in xor steps: the lanes meet five times.
+inline float emu_lane_value(unsigned m, float v, int src) {
+    const int lane = threadIdx.x & 31;
+    float r = 0.f;
+    for (int x = 0; x < 32; ++x) {
+        const float o = __shfl_xor_sync(m, v, x);
+        if ((lane ^ x) == src) r = o;
+    }
+    return r;
+}
+inline float __shfl_up_sync(unsigned m, float v, int off) {
+    const int lane = threadIdx.x & 31;
+    return emu_lane_value(m, v, lane >= off ? lane - off : lane);
+}
+inline float __shfl_sync(unsigned m, float v, int src) { return emu_lane_value(m, v, src); }
 using std::memcpy;
 '''
 
@@ -125,6 +141,56 @@ extern "C" int emu_group_norm(kda::GroupNormParams *p, int bf16, int backward, i
 }
 '''
 
+_RUN_CHUNK = r'''
+#include <sanitizer/asan_interface.h>
+namespace kda { namespace tc { EmuCta *g_cta = nullptr; EmuTf32Slots g_tf32[32]; } }
+static kda::tc::EmuTensorMap emu_map(const void *base, int heads, long long rows, long long ld, bool swizzle) {
+    kda::tc::EmuTensorMap m{};
+    m.base = static_cast<const uint8_t *>(base);
+    m.dims[0] = 128; m.dims[1] = (uint64_t)heads; m.dims[2] = (uint64_t)rows;
+    m.strides[0] = 256; m.strides[1] = (uint64_t)ld * 2;
+    m.box[0] = swizzle ? 64 : 128; m.box[1] = 1; m.box[2] = 64;
+    m.swizzle128 = swizzle ? 1 : 0;
+    return m;
+}
+extern "C" int emu_packed_chunk(kda::PackedParams *pp, int ctas) {
+    using namespace kda;
+    PackedTcParams tp;
+    tp.p = *pp;
+    const tc::EmuTensorMap maps[3] = {emu_map(pp->k, pp->H, pp->T, pp->ldk, true),
+                                      emu_map(pp->q, pp->H, pp->T, pp->ldq, true),
+                                      emu_map(pp->v, pp->HV, pp->T, pp->ldv, false)};
+    for (int i = 0; i < 3; ++i) std::memcpy(&tp.tm[i], &maps[i], sizeof maps[i]);
+    static tc::EmuCta cta;
+    static tc::EmuMBar bars[sizeof smem_raw / 8];
+    cta.smem = smem_raw;
+    cta.smem_bytes = SMEM_BYTES;
+    cta.bars = bars;
+    g_packed_chunk_error = 0;
+    emu_launch_cb(dim3(ctas), dim3(kThreads),
+                  [&](unsigned, unsigned) {
+                      ASAN_UNPOISON_MEMORY_REGION(smem_raw, sizeof smem_raw);
+                      std::memset(cta.tmem, 0xFF, sizeof cta.tmem);
+                      std::memset(smem_raw, 0xFF, sizeof smem_raw);
+                      ASAN_POISON_MEMORY_REGION(smem_raw + SMEM_BYTES, sizeof smem_raw - SMEM_BYTES);
+                      tc::g_cta = &cta;
+                  },
+                  [&] { packed_chunk_kernel(tp); });
+    return (int)g_packed_chunk_error;
+}
+'''
+
+
+def _chunk_unit():
+    s = open(os.path.join(CSRC, "kda_packed_tc.cu")).read()
+    s = s[: s.index("bool packed_chunk_shape")] + "}  // namespace kda\n"
+    s = s.replace("extern __shared__", "extern").replace("__shared__", "static")
+    head = ('#include <functional>\n#include "cuda_runtime.h"\n' + _MORE +
+            "void emu_launch_cb(dim3 grid, dim3 block, const std::function<void(unsigned, unsigned)> &on_block,\n"
+            "                   const std::function<void()> &fn);\n"
+            "namespace kda { namespace { alignas(1024) uint8_t smem_raw[240 * 1024]; } }\n")
+    return head + '#line 1 "kda_packed_tc.cu"\n' + s + _RUN_CHUNK
+
 
 def _unit(src_name, runner, extra=None):
     """As emu_build._unit; `extra` = (from, to): a stretch of the source behind
@@ -147,9 +213,9 @@ def _unit(src_name, runner, extra=None):
 
 def _deps():
     return [os.path.join(CSRC, f) for f in ("kda_packed.cu", "kda_packed_conv.cu", "kda_group_norm.cu",
-                                            "kda_packed.cuh", "kda_group_norm.cuh", "kda_internal.cuh")] + \
+                                            "kda_packed_tc.cu", "kda_packed.cuh", "kda_group_norm.cuh", "kda_internal.cuh")] + \
         [os.path.join(HERE, f) for f in ("emu_packed.py", "emu_build.py", "emu_rt.cpp", "fakeinc/cuda_runtime.h",
-                                         "fakeinc/cuda_bf16.h")]
+                                         "fakeinc/cuda_bf16.h", "tcinc/tc_ptx.cuh")]
 
 
 def build(force=False, sanitizer="address"):
@@ -159,7 +225,8 @@ def build(force=False, sanitizer="address"):
     units = {"emu_packed.cpp": _unit("kda_packed.cu", _RUN_RECURRENT),
              "emu_packed_conv.cpp": _unit("kda_packed_conv.cu", _RUN_CONV),
              "emu_group_norm.cpp": _unit("kda_group_norm.cu", _RUN_NORM,
-                                         ("int pow2_at_least", "cudaError_t launch_group_norm_fwd", True))}
+                                         ("int pow2_at_least", "cudaError_t launch_group_norm_fwd", True)),
+             "emu_packed_chunk.cpp": _chunk_unit()}
     if sanitizer != "address":
         units = {n: t.replace("#include <sanitizer/asan_interface.h>", "#define ASAN_POISON_MEMORY_REGION(a, b)\n"
                               "#define ASAN_UNPOISON_MEMORY_REGION(a, b)") for n, t in units.items()}

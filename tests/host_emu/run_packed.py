@@ -61,6 +61,7 @@ TOL = {"f32": 1e-5, "bf16": 2.0 ** -8 + 1e-5}
 
 PACK = dict(cu=[0, 3, 3, 20, 21, 40], slots=[2, 0, 5, -1, 1], fresh=[0, 1, 1, 0, 0], P=6)
 ODD = dict(cu=[2, 4, 9, 7, 30, 33], slots=[3, 3, 1, 9, 0], fresh=None, P=4)      # repeat, backwards, slot 9
+LONG = dict(cu=[0, 70, 199, 199, 226, 230], slots=[2, 0, 5, -1, 1], fresh=[0, 1, 1, 0, 0], P=6)
 STEP = dict(cu=None, slots=None, fresh=None, P=7)
 
 
@@ -71,7 +72,8 @@ def pack_of(pack, T=None):
     return n, _i32(cu), _i32(pack["slots"]), fresh
 
 
-def run_delta(lib, pack, T, H, HV, Dk, Dv, dtype, gate, per_head, flags=True, pad=0, warps=4, seed=0, check=True):
+def run_delta(lib, pack, T, H, HV, Dk, Dv, dtype, gate, per_head, flags=True, pad=0, warps=4,
+              ctas=0, z_mean=0.0, seed=0, check=True):
     gen = torch.Generator().manual_seed(seed)
     dt = torch.float32 if dtype == "f32" else torch.bfloat16
 
@@ -81,6 +83,7 @@ def run_delta(lib, pack, T, H, HV, Dk, Dv, dtype, gate, per_head, flags=True, pa
 
     gk = () if per_head else (Dk,)
     q, k, v, g, beta = rows(H, Dk), rows(H, Dk), rows(HV, Dv), rows(HV, *gk), rows(HV)
+    g += z_mean
     if not flags:
         g, beta = (g.abs() * -0.3).to(dt), beta.abs().clamp(max=1)
         q, k = (q / Dk ** 0.5).to(dt), (k / Dk ** 0.5).to(dt)
@@ -97,7 +100,11 @@ def run_delta(lib, pack, T, H, HV, Dk, Dv, dtype, gate, per_head, flags=True, pa
                      GATE[gate] if flags else 0, int(per_head), 1 << 30,
                      *(t.stride(0) for t in (q, k, v, g, beta, o)),
                      *map(_ptr, (q, k, v, g, beta, A, b, cu, slots, fresh, pool, o)))
-    word = lib.emu_packed_recurrent(ctypes.byref(p), int(dtype == "bf16"), warps)
+    if ctas:
+        p.split = 0
+        word = lib.emu_packed_chunk(ctypes.byref(p), ctas)
+    else:
+        word = lib.emu_packed_recurrent(ctypes.byref(p), int(dtype == "bf16"), warps)
     if not check:
         return None
     assert bool(word) == packed.live(pack["cu"], pack["slots"], T, pack["P"], n)[1]
@@ -162,6 +169,14 @@ CASES = [
     (run_delta, dict(pack=STEP, T=5, H=2, HV=2, Dk=128, Dv=128, dtype="bf16", gate="bounded", per_head=False)),
     (run_delta, dict(pack=PACK, T=43, H=1, HV=1, Dk=40, Dv=8, dtype="f32", gate="bounded", per_head=True,
                      flags=False, warps=1)),
+    (run_delta, dict(pack=LONG, T=230, H=1, HV=2, Dk=128, Dv=128, dtype="bf16", gate="softplus", per_head=True,
+                     ctas=2)),
+    (run_delta, dict(pack=ODD, T=33, H=1, HV=1, Dk=128, Dv=128, dtype="bf16", gate="bounded", per_head=True, ctas=1,
+                     pad=8)),
+    (run_delta, dict(pack=LONG, T=230, H=1, HV=1, Dk=128, Dv=128, dtype="bf16", gate="softplus", per_head=True,
+                     ctas=3, z_mean=8.0)),
+    (run_delta, dict(pack=LONG, T=230, H=1, HV=1, Dk=128, Dv=128, dtype="bf16", gate="softplus", per_head=True,
+                     flags=False, ctas=1)),
     (run_conv, dict(pack=PACK, T=43, C=128, K=4, dtype="f32", head_dim=128, silu=True, run=1)),
     (run_conv, dict(pack=PACK, T=43, C=384, K=4, dtype="bf16", head_dim=0, silu=True, run=4, pad=8)),
     (run_conv, dict(pack=PACK, T=41, C=128, K=3, dtype="bf16", head_dim=128, silu=False, run=2)),
@@ -177,7 +192,7 @@ CASES = [
     (run_norm, dict(N=1, L=300, C=48, G=1, dtype="bf16", act="none", gated=False, params=False)),
     (run_norm, dict(N=2, L=33, C=18, G=3, dtype="f32", act="sigmoid", gated=False)),
 ]
-RACES = (0, 1, 6, 9, 11, 13, 16)
+RACES = (0, 1, 6, 10, 13, 15, 17, 20)
 
 
 def load(path):
