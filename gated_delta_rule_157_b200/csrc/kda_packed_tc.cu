@@ -18,20 +18,26 @@
 //
 // Precision.  K and Q enter the products as they are given (bf16, unscaled:
 // norms and decays are applied to rows of the fp32 results), so K K^T, Q K^T
-// are exact products.  What is fp32 -- S, R, U and T Diag(beta) -- enters as
-// three bf16 terms (head, middle, tail: 24 bits), six products of (order of
-// magnitude) terms where both sides are split and three where K or Q is the
-// other side; B and its U, which only reach the bf16 output, as two terms and
-// three products.  The state therefore keeps fp32 accuracy over any number of
-// chunks: it lives in fp32 registers, S = gamma S + dS with dS from the MMA.
+// are exact products.  What is fp32 enters as a sum of bf16 terms (head, tail,
+// ...: 8 bits each).  R, U' = Diag(c) U and T Diag(beta) take three terms (24
+// bits), S two where it is multiplied by K or Q (its 2^-18 reaches the state
+// only through U, weighed by the decay; the state itself lives in fp32
+// registers, S = gamma S + dS with dS from the MMA), B and the U of O two (O
+// is rounded to bf16).  Simulated over 16 chunks the state is off by 5e-8 of
+// its norm at decays around e^-1 a token, by 1e-6 with hardly any decay; two
+// terms throughout would leave 3e-6 to 6e-6.
 //
-// One CTA per SM walks (sequence, head) chains: 8 state warps (thread = value
+// One CTA per SM walks (sequence, head) chains.  8 state warps (thread = value
 // channel and half of the key channels; TMEM lane = value channel) run the
-// serial part, 8 prep warps build T Diag(beta), B and the row factors of the
-// next chunk meanwhile.  All MMAs are transposed (D = value channels x tokens
-// or key channels), so S^T, R^T, U^T are A operands in TMEM and K, Q, T, B are
-// B operands in shared memory; the K tile, loaded once by TMA with the 128-byte
-// swizzle, serves K-major (P, K K^T) and MN-major (dS).
+// serial part; two groups of 4 prep warps build T Diag(beta), B and the row
+// factors of the chunks ahead, one the even, the other the odd chunks, so that
+// each has two chunks' time for its chain of small dependent steps.  All MMAs
+// are transposed (D = value channels x tokens or key channels), so S^T, R^T,
+// U^T are A operands in TMEM and K, Q, T, B are B operands in shared memory;
+// the K tile, loaded once by TMA with the 128-byte swizzle, serves K-major
+// (P, K K^T) and MN-major (dS).  Operand terms replace the accumulator columns
+// that the same thread has just read, so the state warps need three barriers a
+// chunk on the serial path.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -44,40 +50,75 @@ namespace {
 using namespace tc;
 
 constexpr int C = 64, D = 128;
-constexpr int kStateThreads = 256, kPrepThreads = 256, kThreads = kStateThreads + kPrepThreads;
+constexpr int kStateThreads = 256, kPrepThreads = 256, kThreads = kStateThreads + kPrepThreads + 128;
+constexpr int kStateWarps = kStateThreads / 32;
+constexpr int kGroup = 128;                // threads of a prep group
 constexpr int LDA = 68;                    // row of the fp32 solve tiles
-constexpr int kPage = 512;                 // sequences scheduled at a time
+constexpr int kPage = 128;                 // sequences scheduled at a time
 
 // Shared memory.
 constexpr uint32_t KQ_BYTES = 32768;       // two blocks of 64 channels x [64 K rows | 64 Q rows] x 128 B
-constexpr uint32_t OFF_KQ = 0;                                   // 2 stages
-constexpr uint32_t OFF_V = OFF_KQ + 2 * KQ_BYTES;                // 2 x [64][128] bf16
-constexpr uint32_t OFF_TB = OFF_V + 2 * 16384;                   // 2 x 3 terms of T Diag(beta), 64 x 64
-constexpr uint32_t OFF_AQK = OFF_TB + 2 * 3 * 8192;              // 2 x 2 terms of B
-constexpr uint32_t OFF_AKK = OFF_AQK + 2 * 2 * 8192;             // A, fp32
-constexpr uint32_t OFF_T = OFF_AKK + C * LDA * 4;                // T and the solve's intermediates, fp32
-constexpr uint32_t OFF_VEC = OFF_T + C * LDA * 4;                // 2 x {fk[64], fq[64], c[64], gamma}
+constexpr int kStages = 3;                 // of K, Q; of B and the row factors
+constexpr uint32_t OFF_KQ = 0;
+constexpr uint32_t OFF_V = OFF_KQ + kStages * KQ_BYTES;        // [64][128] bf16
+constexpr uint32_t OFF_TB = OFF_V + 16384;                       // 3 terms of T Diag(beta), 64 x 64
+constexpr uint32_t OFF_AQK = OFF_TB + 3 * 8192;                  // stages x 2 terms of B
+constexpr uint32_t OFF_A = OFF_AQK + kStages * 2 * 8192;         // per group: A, then T, fp32
+constexpr uint32_t A_BYTES = C * LDA * 4;
+constexpr uint32_t OFF_VEC = OFF_A + 2 * A_BYTES;                // stages x {-fk[64], fq[64], c[64], gamma}
 constexpr uint32_t VEC_BYTES = 1024;
-constexpr uint32_t OFF_PREP = OFF_VEC + 2 * VEC_BYTES;           // G head, G tail, r, rq, beta, norm parts
-constexpr uint32_t OFF_SCHED = OFF_PREP + (5 * 64 + 256) * 4;    // begin, len, slot, order of a page
+constexpr uint32_t OFF_PREP = OFF_VEC + kStages * VEC_BYTES;           // per group: G head, G tail, beta, rk, rq
+constexpr uint32_t PREP_BYTES = 5 * 64 * 4;
+constexpr uint32_t OFF_SCHED = OFF_PREP + 2 * PREP_BYTES;        // begin, len, slot, order of a page
 constexpr uint32_t OFF_MISC = OFF_SCHED + kPage * 16;
 constexpr uint32_t SMEM_USED = OFF_MISC + 256;
 constexpr uint32_t SMEM_BYTES = SMEM_USED + 1024;                // the base is rounded up to 1024
 static_assert(SMEM_BYTES <= 232448, "shared memory of one CTA");
 
-enum { MB_KQ = 0, MB_V = 2, MB_READY = 4, MB_FREE = 6, MB_KK = 8, MB_S = 9, MB_O = 10, MB_DRAIN = 11, kNumBars = 12 };
-constexpr uint32_t MISC_ABORT = 128, MISC_TMEM = 132, MISC_COUNT = 136;
+// Barriers.  KQ, V: loads landed.  READY: prep of a chunk done; FREE: its B and
+// row factors used; TBFREE: its T used.  KK: [K ; Q] K^T done; KKFREE: read.
+// S: P, U, dS done, in turn; O: O done.  From the state warps, one arrival each:
+// ST terms of S written, OT the O before taken, RT terms of R, UT of U and U'.
+enum {
+    MB_KQ = 0, MB_V = 3, MB_READY = 4, MB_FREE = 6, MB_KK = 9, MB_KKFREE = 11, MB_TBFREE = 12, MB_S = 13, MB_O = 14,
+    MB_ST = 15, MB_OT = 16, MB_RT = 17, MB_UT = 18, MB_DRAIN = 19, kNumBars = 20
+};
+__device__ __forceinline__ uint32_t bar_count(int i) {
+    return (i >= MB_FREE && i < MB_KK) || (i >= MB_ST && i <= MB_UT) ? (uint32_t)kStateWarps : 1u;
+}
+constexpr uint32_t MISC_ABORT = 160, MISC_TMEM = 164, MISC_COUNT = 168;
 
-// TMEM columns.
-constexpr uint32_t COL_S = 0;              // S^T: 3 terms x 64; dS overwrites the first 128 once P is done,
-constexpr uint32_t COL_U2 = 128;           // the two terms of U for O the rest
-constexpr uint32_t COL_PK = 192;           // Pk^T, then U^T
-constexpr uint32_t COL_PQ = 256;           // Pq^T, scaled in place, then O^T
-constexpr uint32_t COL_R = 320;            // R^T: 3 terms x 32, then U'^T
-constexpr uint32_t COL_KK = 416;           // [K ; Q] K^T of the next chunk
+// TMEM columns.  16 columns of an fp32 row become 8 + 8 columns of its two terms.
+constexpr uint32_t COL_S = 0;              // S^T: term t of k-step s at 16 s + 8 t; dS
+constexpr uint32_t COL_PK = 128;           // Pk^T; U^T; its two terms as S
+constexpr uint32_t COL_PQ = 192;           // Pq^T
+constexpr uint32_t COL_R = 256;            // R^T, then U'^T: 3 terms x 32
+constexpr uint32_t COL_BU = 352;           // U^T B^T
+constexpr uint32_t COL_KK = 416;           // [K ; Q] K^T of a chunk ahead
 constexpr uint32_t TMEM_COLS = 512;
 
-enum { BAR_STATE = 1, BAR_PREP = 2 };
+enum { BAR_PREP = 1 };                     // + group
+
+// Registers per thread: the state warps hold 64 values of S and a tile with its
+// terms, the prep warps a tile, the issuing warpgroup little.  The shares add up
+// to no more than the block is launched with (640 x 96: the kernel's launch
+// bounds leave 102, allocated in eights) -- an increase beyond that would wait
+// for ever.
+constexpr int kLaunchRegs = 96, kStateRegs = 136, kPrepRegs = 80, kIssueRegs = 48;
+static_assert(kStateThreads * kStateRegs + kPrepThreads * kPrepRegs + 128 * kIssueRegs <= kThreads * kLaunchRegs,
+              "register shares");
+template <int N>
+__device__ __forceinline__ void regs_up() {
+#ifdef __CUDA_ARCH__
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+#endif
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+#ifdef __CUDA_ARCH__
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+#endif
+}
 
 __device__ unsigned int g_packed_chunk_error = 0;
 
@@ -122,45 +163,74 @@ __device__ __forceinline__ uint64_t mn_desc(uint32_t base, uint32_t lbo, int s) 
     return d | (uint64_t)(lbo >> 4) << 16;
 }
 
+// Steps of a descriptor's start address (its low field counts 16 bytes): k-step
+// s of a K-major operand of `rows` rows, and of an MN-major one.
+__host__ __device__ constexpr uint64_t kstep(int rows, int s) { return (uint64_t)(((s >> 2) * rows * 128 + (s & 3) * 32) >> 4); }
+__host__ __device__ constexpr uint64_t mnstep(int s) { return (uint64_t)(s * 2048 >> 4); }
+
 // ---- splits -----------------------------------------------------------------
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-// a, b as N bf16 terms each, rounded to nearest one after another: N = 3 leaves
-// at most 2^-27 of the value, N = 2 2^-18.
+// The pair v as N bf16 terms each, rounded to nearest one after another: N = 3
+// leaves at most 2^-27 of the value, N = 2 2^-18.
 template <int N>
-__device__ __forceinline__ void split2(float a, float b, uint32_t (&w)[N]) {
+__device__ __forceinline__ void split2(float2 v, uint32_t (&w)[N]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        w[i] = pack_bf16x2(a, b);
-        if (i + 1 < N) {
-            a -= bf_lo(w[i]);
-            b -= bf_hi(w[i]);
-        }
+        w[i] = pack_bf16x2(v.x, v.y);
+        if (i + 1 < N) v = __ffma2_rn(make_float2(bf_lo(w[i]), bf_hi(w[i])), make_float2(-1.f, -1.f), v);
     }
 }
-// 32 consecutive columns of an operand row (v0, v1) as N terms at TMEM columns
-// col, col + stride, ...
+// 16 consecutive columns of an operand row as N terms at TMEM columns col,
+// col + stride, ...
 template <int N>
-__device__ __forceinline__ void put_split(uint32_t taddr, uint32_t stride, const float (&v)[32]) {
-    float w[N][16];
+__device__ __forceinline__ void put_split(uint32_t taddr, uint32_t stride, const float2 (&v)[8]) {
+    uint32_t w[N][8];
 #pragma unroll
-    for (int u = 0; u < 16; ++u) {
+    for (int u = 0; u < 8; ++u) {
         uint32_t t[N];
-        split2<N>(v[2 * u], v[2 * u + 1], t);
+        split2<N>(v[u], t);
 #pragma unroll
-        for (int i = 0; i < N; ++i) w[i][u] = __uint_as_float(t[i]);
+        for (int i = 0; i < N; ++i) w[i][u] = t[i];
     }
 #pragma unroll
-    for (int i = 0; i < N; ++i) tmem_st16(taddr + (uint32_t)i * stride, w[i]);
+    for (int i = 0; i < N; ++i) tmem_st8(taddr + (uint32_t)i * stride, w[i]);
 }
-__device__ __forceinline__ void get32(uint32_t taddr, float (&v)[32]) {
-    float a[16], b[16];
-    tmem_ld16x2(taddr, taddr + 16, a, b);
+// The same as two terms over the 16 columns themselves.
+__device__ __forceinline__ void put_two(uint32_t taddr, const float2 (&v)[8]) { put_split<2>(taddr, 8, v); }
+__device__ __forceinline__ void get16(uint32_t taddr, float2 (&v)[8]) {
+    float a[16];
+    tmem_ld16(taddr, a);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        v[i] = a[i];
-        v[16 + i] = b[i];
+    for (int i = 0; i < 8; ++i) v[i] = make_float2(a[2 * i], a[2 * i + 1]);
+}
+// v (.) f, f from shared memory
+__device__ __forceinline__ void scale16(float2 (&v)[8], const float *f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float4 x = *reinterpret_cast<const float4 *>(f + 4 * i);
+        v[2 * i] = __fmul2_rn(v[2 * i], make_float2(x.x, x.y));
+        v[2 * i + 1] = __fmul2_rn(v[2 * i + 1], make_float2(x.z, x.w));
     }
+}
+
+// One lane of the (converged) warp issues; values it needs are made
+// warp-uniform first, so that descriptors are computed on the uniform path.
+__device__ __forceinline__ bool elect_one() {
+#ifdef __CUDA_ARCH__
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(r));
+    return r != 0;
+#else
+    return (threadIdx.x & 31) == 0;
+#endif
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t v) {
+#ifdef __CUDA_ARCH__
+    return __shfl_sync(0xffffffffu, v, 0);
+#else
+    return v;
+#endif
 }
 
 // ---- schedule ---------------------------------------------------------------
@@ -224,29 +294,25 @@ __device__ void fill_page(const PackedParams &p, const Sched &sc, int s0, int ti
 
 // Walks the chunks of this CTA's chains of one page.
 struct Cursor {
-    int items, round;                      // chains of the page; next round to look at
-    int n, chunks;                         // chunk of the chain
-    int seq, begin, len, slot, hv;
+    int round;                             // next round to look at
+    int n, chunks, len;                    // chunk of the chain; chunks and rows of the chain
+    int chain;                             // rank * HV + head
     __device__ __forceinline__ void start(const PackedParams &p, const Sched &sc) {
-        items = *sc.count * p.HV;
         round = 0;
-        n = chunks = 0;
         next_chain(p, sc);
     }
     __device__ __forceinline__ bool valid() const { return n < chunks; }
+    __device__ __forceinline__ int seq(const PackedParams &p, const Sched &sc) const { return sc.order[chain / p.HV]; }
+    __device__ __forceinline__ int head(const PackedParams &p) const { return chain % p.HV; }
+    __device__ __forceinline__ int rows() const { return min(C, len - n * C); }
     __device__ __forceinline__ void next_chain(const PackedParams &p, const Sched &sc) {
-        n = chunks = 0;
-        for (;; ++round) {
-            const long long base = (long long)round * gridDim.x;
-            if (base >= items) return;
-            const long long i = base + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-            if (i >= items) continue;
+        n = chunks = len = 0;
+        const int items = *sc.count * p.HV, ctas = (int)gridDim.x;
+        while (round < (items + ctas - 1) / ctas) {
+            chain = round * ctas + ((round & 1) ? ctas - 1 - (int)blockIdx.x : (int)blockIdx.x);
             ++round;
-            seq = sc.order[(int)i / p.HV];
-            hv = (int)i % p.HV;
-            begin = sc.begin[seq];
-            len = sc.len[seq];
-            slot = sc.slot[seq];
+            if (chain >= items) continue;
+            len = sc.len[seq(p, sc)];
             chunks = (len + C - 1) / C;
             return;
         }
@@ -256,23 +322,26 @@ struct Cursor {
     }
 };
 
-// Loads of one chunk into its stage (one thread).
-__device__ __forceinline__ void request(const PackedParams &p, const CUtensorMap *tm, const Ctx &x, const Cursor &c,
-                                        int stage) {
-    const int row = c.begin + c.n * C, h = c.hv / p.group;
+// Loads of one chunk (one thread).
+__device__ __forceinline__ void request_kq(const PackedParams &p, const CUtensorMap *tm, const Ctx &x, const Sched &sc,
+                                           const Cursor &c, int stage) {
+    const int row = sc.begin[c.seq(p, sc)] + c.n * C, h = c.head(p) / p.group;
     const uint32_t kq = x.sbase + OFF_KQ + (uint32_t)stage * KQ_BYTES, mb = bar_addr(x, MB_KQ + stage);
     mbar_arrive_expect_tx(mb, KQ_BYTES);
     tma_load_3d(kq, &tm[0], 0, h, row, mb);
     tma_load_3d(kq + 16384, &tm[0], 64, h, row, mb);
     tma_load_3d(kq + 8192, &tm[1], 0, h, row, mb);
     tma_load_3d(kq + 16384 + 8192, &tm[1], 64, h, row, mb);
-    const uint32_t mv = bar_addr(x, MB_V + stage);
-    mbar_arrive_expect_tx(mv, 16384);
-    tma_load_3d(x.sbase + OFF_V + (uint32_t)stage * 16384u, &tm[2], 0, c.hv, row, mv);
+}
+__device__ __forceinline__ void request_v(const PackedParams &p, const CUtensorMap *tm, const Ctx &x, const Sched &sc,
+                                          const Cursor &c) {
+    const uint32_t mb = bar_addr(x, MB_V);
+    mbar_arrive_expect_tx(mb, 16384);
+    tma_load_3d(x.sbase + OFF_V, &tm[2], 0, c.head(p), sc.begin[c.seq(p, sc)] + c.n * C, mb);
 }
 
 // =====================================================================
-// Prep role: warps 8-15.
+// Prep role: warps 8-11 the even chunks, warps 12-15 the odd ones.
 // =====================================================================
 __device__ __forceinline__ uint32_t tile_off(int r, int i) {      // 64 x 64 bf16, K-major, swizzled
     return (uint32_t)(r * 128 + (((i >> 3) ^ (r & 7)) << 4) + (i & 7) * 2);
@@ -315,136 +384,132 @@ __device__ __forceinline__ void warp_put(float *Dst, const float d[4], float sgn
     *p0 = v0;
     *p1 = v1;
 }
-// -d (16 x 8, rows row0.., columns col0..) Diag(beta) as the three terms of T Diag(beta).
-__device__ __forceinline__ void warp_tb(uint8_t *tb, int row0, int col0, const float d[4], const float *beta, int lane) {
-    const int g = lane >> 2, t = lane & 3, c = col0 + 2 * t;
-    const float b0 = -beta[c], b1 = -beta[c + 1];
+// Gates of a chunk by one warp: lane = tokens lane, lane + 32.  Requested a
+// chunk of the group ahead and kept as loaded (a conversion would wait).
+struct Gate {
+    __nv_bfloat16 z[2], b[2];
+    float A, bias;
+    int count;                             // rows of the chunk
+    __device__ __forceinline__ void load(const PackedParams &p, const Sched &sc, const Cursor &c, int lane) {
+        count = c.valid() ? c.rows() : 0;
+        A = bias = 0.f;
+        if (count == 0) return;
+        const int hv = c.head(p), row0 = sc.begin[c.seq(p, sc)] + c.n * C;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        uint32_t w[3];
-        split2<3>(d[2 * half] * b0, d[2 * half + 1] * b1, w);
+        for (int u = 0; u < 2; ++u) {
+            const int t = lane + 32 * u;
+            if (t < count) {
+                const long long row = row0 + t;
+                z[u] = static_cast<const __nv_bfloat16 *>(p.g)[row * p.ldg + hv];
+                b[u] = static_cast<const __nv_bfloat16 *>(p.beta)[row * p.ldb + hv];
+            }
+        }
+        if (p.gate_in) {
+            A = p.A_log[hv];
+            if (p.dt_bias) bias = p.dt_bias[hv];
+        }
+    }
+    // Log-decays in log2 units, their running sum as head + tail, and beta.
+    __device__ __forceinline__ void store(const PackedParams &p, int lane, float *gh, float *gl, float *beta) const {
+        const float ea = p.gate_in ? expf(A) : 0.f;
+        float h[2], l[2];
 #pragma unroll
-        for (int i = 0; i < 3; ++i)
-            *reinterpret_cast<uint32_t *>(tb + i * 8192 + tile_off(row0 + g + 8 * half, c)) = w[i];
+        for (int u = 0; u < 2; ++u) {
+            const int t = lane + 32 * u;
+            const float zu = __bfloat162float(z[u]), bu = __bfloat162float(b[u]);
+            float g = p.gate_in ? kda_gate(p.gate_in, zu, bias, ea, p.g_min) : zu;
+            g *= kLog2E;
+            // below 2^-150 a factor is 0 in fp32: a floor keeps the sums finite
+            g = g < -1e4f ? -1e4f : g;
+            g = t < count ? g : 0.f;
+            h[u] = g;
+            beta[t] = t < count ? (p.beta_sigmoid ? sigmoidf_(bu) : bu) : 0.f;
+        }
+        l[0] = l[1] = 0.f;
+        auto add = [](float &ah, float &al, float bh, float bl) {     // (ah, al) += (bh, bl)
+            const float s = ah + bh, v = s - ah;
+            const float e = (ah - (s - v)) + (bh - v) + al + bl;
+            ah = s + e;
+            al = e - (ah - s);
+        };
+#pragma unroll 1
+        for (int off = 1; off < 32; off <<= 1) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const float oh = __shfl_up_sync(0xffffffffu, h[u], off), ol = __shfl_up_sync(0xffffffffu, l[u], off);
+                if (lane >= off) add(h[u], l[u], oh, ol);
+            }
+        }
+        const float th = __shfl_sync(0xffffffffu, h[0], 31), tl = __shfl_sync(0xffffffffu, l[0], 31);
+        add(h[1], l[1], th, tl);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            gh[lane + 32 * u] = h[u];
+            gl[lane + 32 * u] = l[u];
+        }
     }
-}
+};
 
-// One token's log-decay in log2 units, and its beta.
-__device__ __forceinline__ void load_gate(const PackedParams &p, const Cursor &c, int t, float &z, float &b) {
-    z = b = 0.f;
-    if (c.n * C + t < c.len) {
-        const long long row = c.begin + c.n * C + t;
-        z = ld_act(static_cast<const __nv_bfloat16 *>(p.g) + row * p.ldg, c.hv);
-        b = ld_act(static_cast<const __nv_bfloat16 *>(p.beta) + row * p.ldb, c.hv);
-    }
-}
-
-__device__ __forceinline__ void prep_page(const PackedParams &p, const Ctx &x, const Sched &sc, int tid, int &gc) {
+__device__ __forceinline__ void prep_page(const PackedParams &p, const Ctx &x, const Sched &sc, int grp, int tid, int &gc) {
     uint8_t *sm = x.sm;
-    const int lane = tid & 31, warp = tid >> 5;
-    float *gh = reinterpret_cast<float *>(sm + OFF_PREP), *gl = gh + 64, *rk = gl + 64, *rq = rk + 64, *beta = rq + 64;
-    float *part = beta + 64;               // [2][128]
-    float *Akk = reinterpret_cast<float *>(sm + OFF_AKK), *Tm = reinterpret_cast<float *>(sm + OFF_T);
+    const int lane = tid & 31, warp = tid >> 5, bar = BAR_PREP + grp;
+    float *gh = reinterpret_cast<float *>(sm + OFF_PREP + (uint32_t)grp * PREP_BYTES);
+    float *gl = gh + 64, *beta = gl + 64, *rk = beta + 64, *rq = rk + 64;
+    float *Am = reinterpret_cast<float *>(sm + OFF_A + (uint32_t)grp * A_BYTES);
+    uint8_t *tb = sm + OFF_TB;
 
     Cursor cur;
     cur.start(p, sc);
-    float z[2], b[2];                      // gate warp: tokens lane, lane + 32 of the next chunk
-    if (warp == 7 && cur.valid())
-        for (int u = 0; u < 2; ++u) load_gate(p, cur, lane + 32 * u, z[u], b[u]);
+    if ((gc & 1) != grp && cur.valid()) {  // the other group's chunk
+        cur.next(p, sc);
+        ++gc;
+    }
+    Gate gate;
+    if (warp == 3) gate.load(p, sc, cur, lane);
     for (; cur.valid(); ++gc) {
-        const int stage = gc & 1, phase = (gc >> 1) & 1;
-        const int Cc = min(C, cur.len - cur.n * C);
-        uint8_t *kq = sm + OFF_KQ + (uint32_t)stage * KQ_BYTES;
-        uint8_t *tb = sm + OFF_TB + (uint32_t)stage * 3 * 8192, *aqk = sm + OFF_AQK + (uint32_t)stage * 2 * 8192;
+        const int stage = gc % kStages, Cc = cur.rows();
+        const uint8_t *kq = sm + OFF_KQ + (uint32_t)stage * KQ_BYTES;
+        uint8_t *aqk = sm + OFF_AQK + (uint32_t)stage * 2 * 8192;
         float *vec = reinterpret_cast<float *>(sm + OFF_VEC + (uint32_t)stage * VEC_BYTES);
         // A wait that gives up leaves its thread running to the chunk's one vote,
-        // where all return together; until then it issues nothing.
-        bool ok = wait_bar(x, bar_addr(x, MB_KQ + stage), (uint32_t)phase);
-        if (ok && gc >= 2) ok = wait_bar(x, bar_addr(x, MB_FREE + stage), (uint32_t)(((gc - 2) >> 1) & 1));
-        if (Cc < C) {                      // rows behind the sequence: another's, or none
-            for (int i = tid; i < (C - Cc) * 32; i += kPrepThreads) {
-                const int r = Cc + i / 32, q = i % 32;           // 16 chunks of the K row, 16 of the Q row
-                *reinterpret_cast<uint4 *>(kq + ((q >> 3) & 1) * 16384 + (q >> 4) * 8192 + r * 128 + (q & 7) * 16) =
-                    make_uint4(0, 0, 0, 0);
-            }
-            fence_async_smem();
-            named_bar(BAR_PREP, kPrepThreads);
+        // where all return together.
+        bool ok = gc < kStages || wait_bar(x, bar_addr(x, MB_FREE + stage), (uint32_t)((gc / kStages - 1) & 1));
+        if (warp == 3) gate.store(p, lane, gh, gl, beta);
+        cur.next(p, sc);                   // two on: the group's next chunk
+        int step = 1;
+        if (cur.valid()) {
+            cur.next(p, sc);
+            step = 2;
         }
-        if (tid == 0 && ok) {              // [K ; Q] K^T
-            const uint32_t kqa = x.sbase + OFF_KQ + (uint32_t)stage * KQ_BYTES;
-            fence_after_sync();
-#pragma unroll
-            for (int s = 0; s < D / 16; ++s)
-                mma_bf16(x.tm + COL_KK, kmaj_desc(kqa, 128, s), kmaj_desc(kqa, 128, s), idesc_bf16(128, 64), s > 0);
-            mma_commit(bar_addr(x, MB_KK));
-        }
-        // Norms: thread = (row of [K ; Q], block of 64 channels).
+        if (warp == 3) gate.load(p, sc, cur, lane);
+        if (ok) ok = wait_bar(x, bar_addr(x, MB_KQ + stage), (uint32_t)((gc / kStages) & 1));
+        // Norms: thread = row of [K ; Q].
+        float ss;
         {
-            const int r = tid & 127, blk = tid >> 7;
-            float s0 = 0.f, s1 = 0.f;
+            float2 s = make_float2(0.f, 0.f);
             if (p.l2norm) {
+#pragma unroll 4
+                for (int j = 0; j < 16; ++j) {
+                    const uint4 w = *reinterpret_cast<const uint4 *>(kq + (j >> 3) * 16384 + tid * 128 +
+                                                                     (((j & 7) ^ (tid & 7)) << 4));
+                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint4 w = *reinterpret_cast<const uint4 *>(kq + blk * 16384 + r * 128 + ((j ^ (r & 7)) << 4));
-                    s0 = fmaf(bf_lo(w.x), bf_lo(w.x), s0);
-                    s1 = fmaf(bf_hi(w.x), bf_hi(w.x), s1);
-                    s0 = fmaf(bf_lo(w.y), bf_lo(w.y), s0);
-                    s1 = fmaf(bf_hi(w.y), bf_hi(w.y), s1);
-                    s0 = fmaf(bf_lo(w.z), bf_lo(w.z), s0);
-                    s1 = fmaf(bf_hi(w.z), bf_hi(w.z), s1);
-                    s0 = fmaf(bf_lo(w.w), bf_lo(w.w), s0);
-                    s1 = fmaf(bf_hi(w.w), bf_hi(w.w), s1);
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 f = make_float2(bf_lo(u[i]), bf_hi(u[i]));
+                        s = __ffma2_rn(f, f, s);
+                    }
                 }
             }
-            part[blk * 128 + r] = s0 + s1;
+            ss = s.x + s.y;
         }
-        // Gate warp: log-decays in log2 units, their running sum as head + tail.
-        if (warp == 7) {
-            const float ea = p.gate_in ? expf(p.A_log[cur.hv]) : 0.f;
-            const float bias = p.gate_in && p.dt_bias ? p.dt_bias[cur.hv] : 0.f;
-            float h[2], l[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int t = lane + 32 * u;
-                float g = p.gate_in ? kda_gate(p.gate_in, z[u], bias, ea, p.g_min) : z[u];
-                g *= kLog2E;
-                // below 2^-150 a factor is 0 in fp32: a floor keeps the sums finite
-                g = g < -1e4f ? -1e4f : g;
-                h[u] = t < Cc ? g : 0.f;
-                l[u] = 0.f;
-                beta[t] = t < Cc ? (p.beta_sigmoid ? sigmoidf_(b[u]) : b[u]) : 0.f;
-            }
-            auto add = [](float &ah, float &al, float bh, float bl) {     // (ah, al) += (bh, bl)
-                const float s = ah + bh, v = s - ah;
-                const float e = (ah - (s - v)) + (bh - v) + al + bl;
-                ah = s + e;
-                al = e - (ah - s);
-            };
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const float oh = __shfl_up_sync(0xffffffffu, h[u], off), ol = __shfl_up_sync(0xffffffffu, l[u], off);
-                    if (lane >= off) add(h[u], l[u], oh, ol);
-                }
-            }
-            const float th = __shfl_sync(0xffffffffu, h[0], 31), tl = __shfl_sync(0xffffffffu, l[0], 31);
-            add(h[1], l[1], th, tl);
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                gh[lane + 32 * u] = h[u];
-                gl[lane + 32 * u] = l[u];
-            }
-        }
-        named_bar(BAR_PREP, kPrepThreads);
-        if (tid < 128) {                   // row factors
+        named_bar(bar, kGroup);            // the gates
+        {                                  // row factors (0 behind the sequence's end)
             const int t = tid & 63;
-            const float ss = part[tid] + part[128 + tid];
-            const float r = p.l2norm ? (t < Cc ? 1.f / sqrtf(ss + p.l2_eps) : 0.f) : 1.f;
+            const float r = t < Cc ? (p.l2norm ? rsqrtf(ss + p.l2_eps) : 1.f) : 0.f;
             const float e = ex2f_(gh[t] + gl[t]);
             if (tid < 64) {
                 rk[t] = r;
-                vec[t] = r * e;
+                vec[t] = -r * e;
                 vec[128 + t] = r * ex2f_((gh[63] - gh[t]) + (gl[63] - gl[t]));
                 if (t == 0) vec[192] = ex2f_(gh[63] + gl[63]);
             } else {
@@ -452,30 +517,38 @@ __device__ __forceinline__ void prep_page(const PackedParams &p, const Ctx &x, c
                 vec[64 + t] = r * p.scale * e;
             }
         }
-        if (ok) ok = wait_bar(x, bar_addr(x, MB_KK), (uint32_t)(gc & 1));
-        if (named_bar_any(BAR_PREP, kPrepThreads, !ok)) return;
+        if (ok) ok = wait_bar(x, bar_addr(x, MB_KK + grp), (uint32_t)((gc >> 1) & 1));
+        if (named_bar_any(bar, kGroup, !ok)) return;
         fence_after_sync();
-        // A and B from the TMEM product: lane = row of [K ; Q], 32 columns per warp.
+        // A and B from the TMEM product: lane = row of [K ; Q].
         {
-            const int quad = warp & 3, half = warp >> 2, row = (quad & 1) * 32 + lane, j0 = 32 * half;
-            if (!(half == 1 && (quad & 1) == 0)) {               // else wholly above the diagonal
-                float v[32];
-                get32(x.tm + ((uint32_t)(quad * 32) << 16) + COL_KK + (uint32_t)j0, v);
-                const bool is_q = quad >= 2;
-                const float hi = gh[row], lo = gl[row];
-                const float f = is_q ? rq[row] : beta[row] * rk[row];
-                const int last = is_q ? row : row - 1;           // last column that counts
+            const int row = (warp & 1) * 32 + lane;
+            const bool is_q = warp >= 2;
+            const float hi = gh[row], lo = gl[row];
+            const float f = is_q ? rq[row] : beta[row] * rk[row];
+            // the last column that counts; none in rows behind the end, whose products are another's rows
+            const int last = row < Cc ? (is_q ? row : row - 1) : -1;
+#pragma unroll 1
+            for (int j0 = 0; j0 < 32 * (warp & 1) + 32; j0 += 16) {
+                float v[16];
+                tmem_ld16(x.tm + ((uint32_t)(warp * 32) << 16) + COL_KK + (uint32_t)j0, v);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const float e = ex2f_((hi - gh[j0 + j]) + (lo - gl[j0 + j]));
-                    v[j] = j0 + j <= last ? v[j] * (f * rk[j0 + j]) * e : 0.f;
+                for (int j = 0; j < 16; j += 4) {
+                    const float4 h4 = *reinterpret_cast<const float4 *>(gh + j0 + j);
+                    const float4 l4 = *reinterpret_cast<const float4 *>(gl + j0 + j);
+                    const float4 r4 = *reinterpret_cast<const float4 *>(rk + j0 + j);
+                    const float hh[4] = {h4.x, h4.y, h4.z, h4.w}, ll[4] = {l4.x, l4.y, l4.z, l4.w};
+                    const float rr[4] = {r4.x, r4.y, r4.z, r4.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        v[j + i] = j0 + j + i <= last ? v[j + i] * (f * rr[i]) * ex2f_((hi - hh[i]) + (lo - ll[i])) : 0.f;
                 }
                 if (is_q) {
 #pragma unroll
-                    for (int j = 0; j < 32; j += 8) {
+                    for (int j = 0; j < 16; j += 8) {
                         uint32_t w[4][2];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) split2<2>(v[j + 2 * i], v[j + 2 * i + 1], w[i]);
+                        for (int i = 0; i < 4; ++i) split2<2>(make_float2(v[j + 2 * i], v[j + 2 * i + 1]), w[i]);
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
                             *reinterpret_cast<uint4 *>(aqk + i * 8192 + tile_off(row, j0 + j)) =
@@ -483,310 +556,460 @@ __device__ __forceinline__ void prep_page(const PackedParams &p, const Ctx &x, c
                     }
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 32; j += 4)
-                        *reinterpret_cast<float4 *>(Akk + row * LDA + j0 + j) =
-                            make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                    for (int j = 0; j < 16; j += 4)
+                        *reinterpret_cast<float4 *>(Am + row * LDA + j0 + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
                 }
             }
         }
         fence_before_sync();
-        named_bar(BAR_PREP, kPrepThreads);
+        named_bar(bar, kGroup);
+        if (tid == 0) mbar_arrive(bar_addr(x, MB_KKFREE));
+        if (Cc < C) {                      // K and Q rows behind the sequence, another's or none: zero
+            uint8_t *z = sm + OFF_KQ + (uint32_t)stage * KQ_BYTES;
+            for (int i = tid; i < (C - Cc) * 32; i += kGroup) {
+                const int r = Cc + i / 32, q = i % 32;
+                *reinterpret_cast<uint4 *>(z + ((q >> 3) & 1) * 16384 + (q >> 4) * 8192 + r * 128 + (q & 7) * 16) =
+                    make_uint4(0, 0, 0, 0);
+            }
+        }
 
-        cur.next(p, sc);
-        if (warp == 7 && cur.valid())      // in flight during the solve
-            for (int u = 0; u < 2; ++u) load_gate(p, cur, lane + 32 * u, z[u], b[u]);
-
-        // T = (I + A)^-1 by 16 x 16 blocks: the diagonal blocks first, the rest from
-        // T_IJ = -T_II sum_{J<=K<I} A_IK T_KJ in three steps:
+        // T = (I + A)^-1 by 16 x 16 blocks, in place: the diagonal blocks first, the
+        // rest from T_IJ = -T_II sum_{J<=K<I} A_IK T_KJ in three steps:
         //   (1) X10 = A10 T00, X32 = A32 T22, Xc = A_{23,01} T_{01,01} without its T10 term;
         //   (2) T10 = -T11 X10, T32 = -T33 X32, Xc[:, 0:16] -= Xc[:, 16:32] X10
         //       (the missing term A_{23,1} T10 equals -(A_{23,1} T11) X10);
         //   (3) T_{23,01} = -T_{23,23} Xc.
-        // X10, X32 and Xc live above the diagonal of Tm.  (Substitution by blocks,
-        // not powers of A: with keys alike the powers grow and cancel.)
-        if (warp < 2) {
-            const int blk = 2 * warp + (lane >> 4), j = lane & 15;
-            const float *Ab = Akk + 16 * blk * LDA + 16 * blk;
+        // X10, X32 and Xc live above the diagonal.  (Substitution by blocks, not powers
+        // of A: with keys alike the powers grow and cancel.)
+        {
+            // block `warp`, column j = lane % 16 (both half-warps alike), row by row
+            const int j = lane & 15;
+            float *Ab = Am + 16 * warp * LDA + 16 * warp;
             float xs[16];
 #pragma unroll
-            for (int r = 0; r < 16; ++r) xs[r] = 0.f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                xs[i] = i == j ? 1.f : xs[i];                    // rows above j stay 0
-#pragma unroll
-                for (int r = i + 1; r < 16; ++r) xs[r] = fmaf(-Ab[r * LDA + i], xs[i], xs[r]);
-            }
-            const int col = 16 * blk + j;
-            const float bj = beta[col];
-#pragma unroll
             for (int r = 0; r < 16; ++r) {
-                Tm[(16 * blk + r) * LDA + col] = xs[r];
-                uint32_t w[3];
-                split2<3>(xs[r] * bj, 0.f, w);
+                float s0 = r == j ? 1.f : 0.f, s1 = 0.f;
 #pragma unroll
-                for (int i = 0; i < 3; ++i)
-                    *reinterpret_cast<uint16_t *>(tb + i * 8192 + tile_off(16 * blk + r, col)) = (uint16_t)(w[i] & 0xFFFFu);
+                for (int i = 0; i < r; i += 4) {
+                    const float4 a = *reinterpret_cast<const float4 *>(Ab + r * LDA + i);
+                    s0 = fmaf(-a.x, xs[i], s0);
+                    if (i + 1 < r) s1 = fmaf(-a.y, xs[i + 1], s1);
+                    if (i + 2 < r) s0 = fmaf(-a.z, xs[i + 2], s0);
+                    if (i + 3 < r) s1 = fmaf(-a.w, xs[i + 3], s1);
+                }
+                xs[r] = s0 + s1;
+            }
+            __syncwarp();                  // every row of the block has been read
+            if (lane < 16) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) Ab[r * LDA + j] = xs[r];
             }
         }
-        named_bar(BAR_PREP, kPrepThreads);
-        for (int task = warp; task < 12; task += 8) {
+        named_bar(bar, kGroup);
+#pragma unroll 1
+        for (int task = warp; task < 12; task += 4) {
             const int blk = task >> 1, nh = (task & 1) * 8;
             const int arow = blk == 0 ? 16 : blk == 1 ? 48 : (blk == 2 || blk == 4) ? 32 : 48;
             const int kc = blk == 1 ? 32 : (blk == 2 || blk == 3) ? 16 : 0;
             const int drow = blk == 1 ? 32 : (blk == 3 || blk == 5) ? 16 : 0;
             const int dcol = blk == 0 ? 16 : (blk == 4 || blk == 5) ? 32 : 48;
             float d[4] = {0.f, 0.f, 0.f, 0.f};
-            warp_mm<2>(d, Akk + arow * LDA + kc, Tm + kc * LDA + kc + nh, lane);
-            warp_put(Tm + drow * LDA + dcol + nh, d, 1.f, false, lane);
+            warp_mm<2>(d, Am + arow * LDA + kc, Am + kc * LDA + kc + nh, lane);
+            warp_put(Am + drow * LDA + dcol + nh, d, 1.f, false, lane);
         }
-        named_bar(BAR_PREP, kPrepThreads);
-        {
-            const int task = warp >> 1, nh = (warp & 1) * 8;
-            const int arow = task == 0 ? 16 : task == 1 ? 48 : 16 * (task - 2);
-            const int acol = task == 0 ? 16 : 48;
-            const int brow = task == 1 ? 32 : 0, bcol = task == 1 ? 48 : 16;
-            const int drow = task == 0 ? 16 : task == 1 ? 48 : 16 * (task - 2);
-            const int dcol = task == 0 ? 0 : 32;
+        named_bar(bar, kGroup);
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {      // warp = task, both halves of its columns
+            const int nh = 8 * i;
+            const int arow = warp == 0 ? 16 : warp == 1 ? 48 : 16 * (warp - 2);
+            const int acol = warp == 0 ? 16 : 48;
+            const int brow = warp == 1 ? 32 : 0, bcol = warp == 1 ? 48 : 16;
+            const int drow = warp == 0 ? 16 : warp == 1 ? 48 : 16 * (warp - 2);
+            const int dcol = warp == 0 ? 0 : 32;
             float d[4] = {0.f, 0.f, 0.f, 0.f};
-            warp_mm<2>(d, Tm + arow * LDA + acol, Tm + brow * LDA + bcol + nh, lane);
-            if (task != 0) warp_put(Tm + drow * LDA + dcol + nh, d, -1.f, task >= 2, lane);
-            if (task < 2) warp_tb(tb, drow, dcol + nh, d, beta, lane);       // T10, T32
+            warp_mm<2>(d, Am + arow * LDA + acol, Am + brow * LDA + bcol + nh, lane);
+            warp_put(Am + drow * LDA + dcol + nh, d, -1.f, warp >= 2, lane);
         }
-        named_bar(BAR_PREP, kPrepThreads);
-        {
-            const int mt = warp >> 2, n0 = 8 * (warp & 3);
+        named_bar(bar, kGroup);
+#pragma unroll 1
+        for (int mt = 0; mt < 2; ++mt) {   // warp = columns 8 warp ..
             float d[4] = {0.f, 0.f, 0.f, 0.f};
-            const float *A = Tm + (32 + 16 * mt) * LDA + 32, *B = Tm + 32 + n0;
-            if (mt == 0) warp_mm<2>(d, A, B, lane);
-            else warp_mm<4>(d, A, B, lane);
-            warp_tb(tb, 32 + 16 * mt, n0, d, beta, lane);
+            const float *A = Am + (32 + 16 * mt) * LDA + 32, *B = Am + 32 + 8 * warp;
+            warp_mm<2>(d, A, B, lane);
+            if (mt == 1) warp_mm<2>(d, A + 16, B + 16 * LDA, lane);
+            warp_put(Am + (32 + 16 * mt) * LDA + 8 * warp, d, -1.f, false, lane);
+        }
+        if (ok && gc > 0) ok = wait_bar(x, bar_addr(x, MB_TBFREE), (uint32_t)((gc - 1) & 1));
+        named_bar(bar, kGroup);
+        {                                  // T Diag(beta) as three terms: warp = block row, lane pair = row
+            const int r = tid >> 1;
+#pragma unroll 1
+            for (int c0 = 8 * (tid & 1); c0 < 16 * warp + 16; c0 += 16) {
+                const float4 t0 = *reinterpret_cast<const float4 *>(Am + r * LDA + c0);
+                const float4 t1 = *reinterpret_cast<const float4 *>(Am + r * LDA + c0 + 4);
+                const float4 b0 = *reinterpret_cast<const float4 *>(beta + c0);
+                const float4 b1 = *reinterpret_cast<const float4 *>(beta + c0 + 4);
+                uint32_t w[4][3];
+                split2<3>(__fmul2_rn(make_float2(t0.x, t0.y), make_float2(b0.x, b0.y)), w[0]);
+                split2<3>(__fmul2_rn(make_float2(t0.z, t0.w), make_float2(b0.z, b0.w)), w[1]);
+                split2<3>(__fmul2_rn(make_float2(t1.x, t1.y), make_float2(b1.x, b1.y)), w[2]);
+                split2<3>(__fmul2_rn(make_float2(t1.z, t1.w), make_float2(b1.z, b1.w)), w[3]);
+#pragma unroll
+                for (int i = 0; i < 3; ++i)
+                    *reinterpret_cast<uint4 *>(tb + i * 8192 + tile_off(r, c0)) =
+                        make_uint4(w[0][i], w[1][i], w[2][i], w[3][i]);
+            }
+        }
+        if (Cc < C) {                      // V rows behind the sequence
+            if (ok) ok = wait_bar(x, bar_addr(x, MB_V), (uint32_t)(gc & 1));
+            for (int i = tid; i < (C - Cc) * 16; i += kGroup)
+                *reinterpret_cast<uint4 *>(sm + OFF_V + (Cc + i / 16) * 256 + (i % 16) * 16) = make_uint4(0, 0, 0, 0);
         }
         fence_async_smem();
-        named_bar(BAR_PREP, kPrepThreads);
-        if (tid == 0) mbar_arrive(bar_addr(x, MB_READY + stage));
+        named_bar(bar, kGroup);
+        if (tid == 0 && ok) mbar_arrive(bar_addr(x, MB_READY + grp));
+        gc += step - 1;
     }
 }
 
 // =====================================================================
 // State role: warps 0-7.  Thread = (TMEM lane = value channel j, half hf).
 // =====================================================================
-struct StateRole {
-    float S[64];                           // S[64 hf + i][j]
-    uint32_t o[16];                        // the last chunk's outputs, token pairs, as bf16
-    long long o_row;                       // their first row, and how many of the 64 count
-    int o_count, o_hv;
+// One chain's S and where its outputs go.
+struct Chain {
+    float *pool;                           // S[64 hf][j] of the slot
+    __nv_bfloat16 *o;                      // of this lane: row 32 hf + (lane & 1), channels j & ~1 and the next
+    bool zero;
+    __device__ __forceinline__ void at(const PackedParams &p, const Sched &sc, const Cursor &c, int s0, int hf, int j) {
+        const int seq = c.seq(p, sc), hv = c.head(p);
+        pool = p.pool + (((size_t)sc.slot[seq] * p.HV + hv) * D + 64 * hf) * D + j;
+        o = static_cast<__nv_bfloat16 *>(p.o) + ((long long)sc.begin[seq] + 32 * hf + (j & 1)) * p.ldo +
+            (long long)hv * D + (j & ~1);
+        zero = p.fresh && p.fresh[s0 + seq];
+    }
 };
-
-__device__ __forceinline__ void store_o(const PackedParams &p, const StateRole &st, int hf, int j) {
-    if (st.o_count == 0) return;
-    // lanes exchange so that each writes two channels of one token of the pair
-    const bool odd = j & 1;
-    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.o) + st.o_row * p.ldo + (long long)st.o_hv * D + (j & ~1);
+__device__ __forceinline__ void load_state(const Chain &ch, float2 (&S)[32]) {
 #pragma unroll
-    for (int u = 0; u < 16; ++u) {
-        const uint32_t mine = st.o[u];
-        const uint32_t other = __float_as_uint(__shfl_xor_sync(0xffffffffu, __uint_as_float(mine), 1));
-        const uint32_t w = odd ? (other >> 16) | (mine & 0xFFFF0000u) : (mine & 0xFFFFu) | (other << 16);
-        const int t = 32 * hf + 2 * u + (odd ? 1 : 0);
-        if (t < st.o_count) *reinterpret_cast<uint32_t *>(o + (long long)t * p.ldo) = w;
+    for (int i = 0; i < 32; ++i)
+        S[i] = ch.zero ? make_float2(0.f, 0.f) : make_float2(ch.pool[(2 * i) * D], ch.pool[(2 * i + 1) * D]);
+}
+__device__ __forceinline__ void put_state(uint32_t tl, int hf, const float2 (&S)[32]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        float2 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = S[8 * q + i];
+        put_two(tl + COL_S + (uint32_t)(64 * hf + 16 * q), v);
     }
 }
 
-__device__ __forceinline__ void load_state(const PackedParams &p, const Cursor &c, int s0, int hf, int j, float (&S)[64]) {
-    const bool zero = p.fresh && p.fresh[s0 + c.seq];
-    const float *src = p.pool + (((size_t)c.slot * p.HV + c.hv) * D + 64 * hf) * D + j;
-#pragma unroll
-    for (int i = 0; i < 64; ++i) S[i] = zero ? 0.f : src[(size_t)i * D];
-}
-__device__ __forceinline__ void put_state(uint32_t tl, int hf, const float (&S)[64]) {
+// O^T = Pq^T Diag(fq) + U^T B^T of a chunk, as bf16 pairs of tokens.
+__device__ __forceinline__ void take_o(uint32_t tl, int hf, const float *fq, uint32_t (&o)[16]) {
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-        float v[32];
+        float a[16], b[16];
+        tmem_ld16x2(tl + COL_PQ + (uint32_t)(32 * hf + 16 * q), tl + COL_BU + (uint32_t)(32 * hf + 16 * q), a, b);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = S[32 * q + i];
-        put_split<3>(tl + COL_S + (uint32_t)(32 * hf + 16 * q), 64, v);
+        for (int u = 0; u < 4; ++u) {
+            const float4 f = *reinterpret_cast<const float4 *>(fq + 16 * q + 4 * u);
+            const float2 o0 = __ffma2_rn(make_float2(a[4 * u], a[4 * u + 1]), make_float2(f.x, f.y),
+                                         make_float2(b[4 * u], b[4 * u + 1]));
+            const float2 o1 = __ffma2_rn(make_float2(a[4 * u + 2], a[4 * u + 3]), make_float2(f.z, f.w),
+                                         make_float2(b[4 * u + 2], b[4 * u + 3]));
+            o[8 * q + 2 * u] = pack_bf16x2(o0.x, o0.y);
+            o[8 * q + 2 * u + 1] = pack_bf16x2(o1.x, o1.y);
+        }
+    }
+}
+// Lanes exchange so that each writes two channels of one token of a pair;
+// `count` of the 32 tokens are rows.
+__device__ __forceinline__ void store_o(const PackedParams &p, __nv_bfloat16 *at, int count, int lane,
+                                        const uint32_t (&o)[16]) {
+    if (count <= 0) return;
+    const uint32_t sel = (lane & 1) ? 0x3276u : 0x5410u;         // odd: other's upper, mine; even: mine, other's lower
+    const int first = lane & 1;
+#pragma unroll
+    for (int u = 0; u < 16; ++u) {
+        const uint32_t other = __float_as_uint(__shfl_xor_sync(0xffffffffu, __uint_as_float(o[u]), 1));
+        const uint32_t w = __byte_perm(o[u], other, sel);
+        if (2 * u + first < count) *reinterpret_cast<uint32_t *>(at) = w;
+        at += 2 * p.ldo;
     }
 }
 
-// Runs the page's chunks; `ph` counts the phases of MB_S, `requested` (thread 0)
-// the chunks loaded.
-__device__ __forceinline__ void state_page(const PackedParams &p, const CUtensorMap *tmaps, const Ctx &x,
-                                           const Sched &sc, int s0, int tid, int &gc, uint32_t &ph, int &requested) {
-    uint8_t *sm = x.sm;
-    const int warp = tid >> 5, hf = warp >> 2, j = (warp & 3) * 32 + (tid & 31);
-    const uint32_t tl = x.tm + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t id_p = idesc_bf16(128, 128), id_u = idesc_bf16(128, 64);
-    const uint32_t id_s = idesc_bf16(128, 128, false, /*b_mn_major=*/true);
-
-    Cursor cur, ahead;
-    cur.start(p, sc);
-    if (!cur.valid()) return;
-    ahead = cur;
-    if (tid == 0) {                        // two chunks in flight from the start
-        for (int i = 0; i < 2 && ahead.valid(); ++i) {
-            request(p, tmaps, x, ahead, (gc + i) & 1);
-            ++requested;
-            ahead.next(p, sc);
-        }
-    }
-    StateRole st;
-    st.o_count = 0;
-    load_state(p, cur, s0, hf, j, st.S);
-    put_state(tl, hf, st.S);
+// One arrival of the (converged) warp, after what its lanes wrote to TMEM.
+__device__ __forceinline__ void warp_arrive(const Ctx &x, int bar, int lane) {
     tmem_st_wait();
     fence_before_sync();
-    named_bar(BAR_STATE, kStateThreads);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_addr(x, bar));
+}
 
+// Runs the page's chunks; `gc` counts this CTA's chunks, `ph` the phases of MB_S.
+// The warps do not wait for one another: what one lane reads of TMEM it wrote
+// itself or an MMA did.  A warp whose wait gives up returns; the abort flag ends
+// the others' waits.
+__device__ __forceinline__ void state_page(const PackedParams &p, const Ctx &x, const Sched &sc, int s0, int tid, int &gc,
+                                           uint32_t &ph) {
+    uint8_t *sm = x.sm;
+    const int warp = tid >> 5, lane = tid & 31, hf = warp >> 2, j = (warp & 3) * 32 + lane;
+    const uint32_t tl = x.tm + ((uint32_t)((warp & 3) * 32) << 16);
+
+    Cursor cur;
+    cur.start(p, sc);
+    if (!cur.valid()) return;
+    float2 S[32];                          // S[64 hf + 2 i .. + 1][j]
+    Chain ch;
+    ch.at(p, sc, cur, s0, hf, j);
+    load_state(ch, S);
+    put_state(tl, hf, S);
+    warp_arrive(x, MB_ST, lane);
+    __nv_bfloat16 *o_at = nullptr;         // of the chunk before, and its rows of this half
+    int o_count = 0;
+
+    bool first = true;
     for (; cur.valid(); ++gc) {
-        const int stage = gc & 1;
-        const uint32_t phase = (uint32_t)((gc >> 1) & 1);
-        const int Cc = min(C, cur.len - cur.n * C);
-        const uint32_t kq = x.sbase + OFF_KQ + (uint32_t)stage * KQ_BYTES;
-        const float *vec = reinterpret_cast<const float *>(sm + OFF_VEC + (uint32_t)stage * VEC_BYTES);
-        // (waits that give up: as in prep_page)
-        bool ok = wait_bar(x, bar_addr(x, MB_READY + stage), phase);
-        if (tid == 0 && ok) {              // P^T = S^T [K ; Q]^T, small terms first
+        const int stage = gc % kStages, before = (gc + kStages - 1) % kStages;
+        const float *vec = reinterpret_cast<const float *>(sm + OFF_VEC + (uint32_t)stage * VEC_BYTES) + 32 * hf;
+        if (!first) {                      // O of the chunk before
+            uint32_t o[16];
+            if (!wait_bar(x, bar_addr(x, MB_O), (uint32_t)((gc - 1) & 1))) return;
             fence_after_sync();
-#pragma unroll
-            for (int t = 2; t >= 0; --t)
-#pragma unroll
-                for (int s = 0; s < D / 16; ++s)
-                    mma_bf16_tmem_a(x.tm + COL_PK, x.tm + COL_S + (uint32_t)(64 * t + 8 * s), kmaj_desc(kq, 128, s), id_p,
-                                    t < 2 || s > 0);
-            mma_commit(bar_addr(x, MB_S));
+            take_o(tl, hf, reinterpret_cast<const float *>(sm + OFF_VEC + (uint32_t)before * VEC_BYTES) + 64 + 32 * hf, o);
+            warp_arrive(x, MB_OT, lane);
+            if (lane == 0) mbar_arrive(bar_addr(x, MB_FREE + before));
+            store_o(p, o_at, o_count, lane, o);
+        } else {
+            warp_arrive(x, MB_OT, lane);
         }
-        store_o(p, st, hf, j);             // the previous chunk's
-        if (ok) ok = wait_bar(x, bar_addr(x, MB_V + stage), phase);
-        uint32_t vv[16];
-        {
-            const uint8_t *vt = sm + OFF_V + (uint32_t)stage * 16384u + (uint32_t)(32 * hf) * 256u + 2u * (uint32_t)j;
-#pragma unroll
-            for (int u = 0; u < 16; ++u)
-                vv[u] = (uint32_t)*reinterpret_cast<const uint16_t *>(vt + 512 * u) |
-                        (uint32_t)*reinterpret_cast<const uint16_t *>(vt + 512 * u + 256) << 16;
-        }
-        if (ok) ok = wait_bar(x, bar_addr(x, MB_S), ph);
+        if (!wait_bar(x, bar_addr(x, MB_READY + (gc & 1)), (uint32_t)((gc >> 1) & 1))) return;
+        if (!wait_bar(x, bar_addr(x, MB_V), (uint32_t)(gc & 1))) return;
+        if (!wait_bar(x, bar_addr(x, MB_S), ph)) return;
         ph ^= 1u;
         fence_after_sync();
-        {                                  // R^T = V^T - Pk^T Diag(fk)
-            float v[32];
-            get32(tl + COL_PK + (uint32_t)(32 * hf), v);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const float vi = (i & 1) ? bf_hi(vv[i >> 1]) : bf_lo(vv[i >> 1]);
-                v[i] = 32 * hf + i < Cc ? fmaf(-vec[32 * hf + i], v[i], vi) : 0.f;
-            }
-            put_split<3>(tl + COL_R + (uint32_t)(16 * hf), 32, v);
-        }
-        tmem_st_wait();
-        fence_before_sync();
-        named_bar(BAR_STATE, kStateThreads);
-        if (tid == 0 && ok) {              // U^T = R^T (T Diag(beta))^T
-            fence_after_sync();
-            const uint32_t tb = x.sbase + OFF_TB + (uint32_t)stage * 3 * 8192;
-            const int ra[6] = {2, 1, 0, 1, 0, 0}, ta[6] = {0, 1, 2, 0, 1, 0};
-#pragma unroll
-            for (int t = 0; t < 6; ++t)
-#pragma unroll
-                for (int s = 0; s < C / 16; ++s)
-                    mma_bf16_tmem_a(x.tm + COL_PK, x.tm + COL_R + (uint32_t)(32 * ra[t] + 8 * s),
-                                    kmaj_desc(tb + (uint32_t)ta[t] * 8192u, 64, s), id_u, t > 0 || s > 0);
-            mma_commit(bar_addr(x, MB_S));
-        }
-        {                                  // meanwhile Pq^T Diag(fq), in place
-            float v[32];
-            get32(tl + COL_PQ + (uint32_t)(32 * hf), v);
-            float a[16], b[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                a[i] = v[i] * vec[64 + 32 * hf + i];
-                b[i] = v[16 + i] * vec[64 + 32 * hf + 16 + i];
-            }
-            tmem_st16(tl + COL_PQ + (uint32_t)(32 * hf), a);
-            tmem_st16(tl + COL_PQ + (uint32_t)(32 * hf + 16), b);
-        }
-        if (ok) ok = wait_bar(x, bar_addr(x, MB_S), ph);
-        ph ^= 1u;
-        fence_after_sync();
-        {                                  // U as two terms for O, Diag(c) U as three for dS
-            float v[32];
-            get32(tl + COL_PK + (uint32_t)(32 * hf), v);
-            put_split<2>(tl + COL_U2 + (uint32_t)(16 * hf), 32, v);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] *= vec[128 + 32 * hf + i];
-            put_split<3>(tl + COL_R + (uint32_t)(16 * hf), 32, v);
-        }
-        const float gamma = vec[192];
-        tmem_st_wait();
-        fence_before_sync();
-        named_bar(BAR_STATE, kStateThreads);
-        if (tid == 0 && ok) {              // dS^T = U'^T K, then O^T += U^T B^T
-            fence_after_sync();
-#pragma unroll
-            for (int t = 2; t >= 0; --t)
-#pragma unroll
-                for (int s = 0; s < C / 16; ++s)
-                    mma_bf16_tmem_a(x.tm + COL_S, x.tm + COL_R + (uint32_t)(32 * t + 8 * s), mn_desc(kq, 16384, s), id_s,
-                                    t < 2 || s > 0);
-            mma_commit(bar_addr(x, MB_S));
-            const uint32_t aq = x.sbase + OFF_AQK + (uint32_t)stage * 2 * 8192;
-            const int ua[3] = {1, 0, 0}, ba[3] = {0, 1, 0};
-#pragma unroll
-            for (int t = 0; t < 3; ++t)
-#pragma unroll
-                for (int s = 0; s < C / 16; ++s)
-                    mma_bf16_tmem_a(x.tm + COL_PQ, x.tm + COL_U2 + (uint32_t)(32 * ua[t] + 8 * s),
-                                    kmaj_desc(aq + (uint32_t)ba[t] * 8192u, 64, s), id_u, 1u);
-            mma_commit(bar_addr(x, MB_O));
-        }
-        if (ok) ok = wait_bar(x, bar_addr(x, MB_S), ph);
-        ph ^= 1u;
-        fence_after_sync();
-#pragma unroll
+        // R^T = V^T - Pk^T Diag(fk)  (vec holds -fk)
+        const uint8_t *vt = sm + OFF_V + (uint32_t)(32 * hf) * 256u + 2u * (uint32_t)j;
+#pragma unroll 1
         for (int q = 0; q < 2; ++q) {
-            float v[32];
-            get32(tl + COL_S + (uint32_t)(64 * hf + 32 * q), v);
+            float2 v[8], pk[8];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) st.S[32 * q + i] = fmaf(gamma, st.S[32 * q + i], v[i]);
-        }
-        if (ok) ok = wait_bar(x, bar_addr(x, MB_O), (uint32_t)(gc & 1));
-        fence_after_sync();
-        {
-            float v[32];
-            get32(tl + COL_PQ + (uint32_t)(32 * hf), v);
+            for (int u = 0; u < 8; ++u)
+                v[u] = make_float2(bf_lo(*reinterpret_cast<const uint16_t *>(vt + 4096 * q + 512 * u)),
+                                   bf_lo(*reinterpret_cast<const uint16_t *>(vt + 4096 * q + 512 * u + 256)));
+            get16(tl + COL_PK + (uint32_t)(32 * hf + 16 * q), pk);
 #pragma unroll
-            for (int u = 0; u < 16; ++u) st.o[u] = pack_bf16x2(v[2 * u], v[2 * u + 1]);
-        }
-        st.o_row = cur.begin + cur.n * C;
-        st.o_count = Cc;
-        st.o_hv = cur.hv;
-        fence_before_sync();
-        if (named_bar_any(BAR_STATE, kStateThreads, !ok)) return;
-        if (tid == 0) {                    // every operand of this chunk has been read
-            mbar_arrive(bar_addr(x, MB_FREE + stage));
-            if (ahead.valid()) {
-                request(p, tmaps, x, ahead, stage);
-                ++requested;
-                ahead.next(p, sc);
+            for (int u = 0; u < 4; ++u) {
+                const float4 f = *reinterpret_cast<const float4 *>(vec + 16 * q + 4 * u);
+                v[2 * u] = __ffma2_rn(make_float2(f.x, f.y), pk[2 * u], v[2 * u]);
+                v[2 * u + 1] = __ffma2_rn(make_float2(f.z, f.w), pk[2 * u + 1], v[2 * u + 1]);
             }
+            put_split<3>(tl + COL_R + (uint32_t)(16 * hf + 8 * q), 32, v);
+        }
+        warp_arrive(x, MB_RT, lane);
+        if (!wait_bar(x, bar_addr(x, MB_S), ph)) return;
+        ph ^= 1u;
+        fence_after_sync();
+#pragma unroll 1
+        for (int q = 0; q < 2; ++q) {      // U as two terms for O, Diag(c) U as three for dS
+            float2 v[8];
+            const uint32_t at = tl + COL_PK + (uint32_t)(32 * hf + 16 * q);
+            get16(at, v);
+            put_two(at, v);
+            scale16(v, vec + 128 + 16 * q);
+            put_split<3>(tl + COL_R + (uint32_t)(16 * hf + 8 * q), 32, v);
+        }
+        const float gamma = vec[192 - 32 * hf];
+        warp_arrive(x, MB_UT, lane);
+        o_at = ch.o + (long long)cur.n * C * p.ldo;
+        o_count = cur.rows() - 32 * hf;
+        if (!wait_bar(x, bar_addr(x, MB_S), ph)) return;
+        ph ^= 1u;
+        fence_after_sync();
+        // S = gamma S + dS, and its terms over the columns of dS
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            float2 v[8];
+            const uint32_t at = tl + COL_S + (uint32_t)(64 * hf + 16 * q);
+            get16(at, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                S[8 * q + i] = __ffma2_rn(make_float2(gamma, gamma), S[8 * q + i], v[i]);
+                v[i] = S[8 * q + i];
+            }
+            put_two(at, v);
         }
         const bool last = cur.n + 1 == cur.chunks;
         if (last) {
-            float *dst = p.pool + (((size_t)cur.slot * p.HV + cur.hv) * D + 64 * hf) * D + j;
 #pragma unroll
-            for (int i = 0; i < 64; ++i) dst[(size_t)i * D] = st.S[i];
+            for (int i = 0; i < 32; ++i) {
+                ch.pool[(2 * i) * D] = S[i].x;
+                ch.pool[(2 * i + 1) * D] = S[i].y;
+            }
         }
         cur.next(p, sc);
+        first = false;
         if (cur.valid()) {
-            if (last) load_state(p, cur, s0, hf, j, st.S);
-            fence_after_sync();
-            put_state(tl, hf, st.S);
-            tmem_st_wait();
-            fence_before_sync();
-            named_bar(BAR_STATE, kStateThreads);
+            if (last) {
+                ch.at(p, sc, cur, s0, hf, j);
+                load_state(ch, S);
+                put_state(tl, hf, S);
+            }
+            warp_arrive(x, MB_ST, lane);
         }
     }
-    store_o(p, st, hf, j);
+    if (!wait_bar(x, bar_addr(x, MB_O), (uint32_t)((gc - 1) & 1))) return;
+    fence_after_sync();
+    uint32_t o[16];
+    take_o(tl, hf, reinterpret_cast<const float *>(sm + OFF_VEC + (uint32_t)((gc - 1) % kStages) * VEC_BYTES) + 64 + 32 * hf, o);
+    fence_before_sync();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_addr(x, MB_FREE + (gc - 1) % kStages));
+    store_o(p, o_at, o_count, lane, o);
+}
+
+// =====================================================================
+// Issuing warp: loads and MMAs, one elected lane, in the order the chunks need
+// them.  The product for the prep warps goes last in a chunk, where the tensor
+// pipe waits for the state warps.
+// =====================================================================
+struct Issue {
+    int kq_n, v_n, kk_n;                   // chunks of this CTA requested, and multiplied for the prep warps
+    uint32_t ph;                           // phases of MB_S
+};
+
+// [K ; Q] K^T of chunk n, once its rows have landed and the product before it has been read.
+__device__ __forceinline__ bool issue_kk(const Ctx &x, Issue &is) {
+    const int n = is.kk_n++;
+    if (!wait_bar(x, bar_addr(x, MB_KQ + n % kStages), (uint32_t)((n / kStages) & 1))) return false;
+    if (n > 0 && !wait_bar(x, bar_addr(x, MB_KKFREE), (uint32_t)((n - 1) & 1))) return false;
+    const uint32_t a = uniform(x.sbase + OFF_KQ + (uint32_t)(n % kStages) * KQ_BYTES), d = uniform(x.tm + COL_KK);
+    const uint32_t mb = uniform(bar_addr(x, MB_KK + (n & 1)));
+    if (elect_one()) {
+        fence_after_sync();
+        const uint64_t dk = kmaj_desc(a, 128, 0);
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s)
+            mma_bf16(d, dk + kstep(128, s), dk + kstep(128, s), idesc_bf16(128, 64), s > 0);
+        mma_commit(mb);
+    }
+    __syncwarp();
+    return true;
+}
+
+__device__ __forceinline__ void issue_page(const PackedParams &p, const CUtensorMap *tmaps, const Ctx &x, const Sched &sc,
+                                           int &gc, Issue &is) {
+    const uint32_t id_u = idesc_bf16(128, 64), id_s = idesc_bf16(128, 128, false, /*b_mn_major=*/true);
+    const uint32_t tm = uniform(x.tm), mb = uniform(bar_addr(x, MB_S)), mo = uniform(bar_addr(x, MB_O));
+    const uint32_t mt = uniform(bar_addr(x, MB_TBFREE)), tb = uniform(x.sbase + OFF_TB);
+    Cursor cur, kq, v;                     // the chunk at hand, the next K and Q, the next V to load
+    cur.start(p, sc);
+    if (!cur.valid()) return;
+    kq = v = cur;
+    int left = 0;                          // chunks of the page whose product is not issued yet
+    for (Cursor c = cur; c.valid(); c.next_chain(p, sc)) left += c.chunks;
+    auto load_kq = [&]() {
+        if (!kq.valid()) return;
+        if (elect_one()) request_kq(p, tmaps, x, sc, kq, is.kq_n % kStages);
+        __syncwarp();
+        ++is.kq_n;
+        kq.next(p, sc);
+    };
+    auto load_v = [&]() {
+        if (!v.valid()) return;
+        if (elect_one()) request_v(p, tmaps, x, sc, v);
+        __syncwarp();
+        ++is.v_n;
+        v.next(p, sc);
+    };
+    for (int i = 0; i < kStages; ++i) load_kq();
+    load_v();
+    for (int i = 0; i < 2 && left > 0; ++i, --left)
+        if (!issue_kk(x, is)) return;
+    for (bool first = true; cur.valid(); first = false, ++gc, cur.next(p, sc)) {
+        const uint32_t par = (uint32_t)(gc & 1);
+        const uint32_t a = uniform(x.sbase + OFF_KQ + (uint32_t)(gc % kStages) * KQ_BYTES);
+        const uint32_t aq = uniform(x.sbase + OFF_AQK + (uint32_t)(gc % kStages) * 2 * 8192);
+        // Pk^T = S^T K^T, small terms first; its columns still hold the U of the O before
+        if (!wait_bar(x, bar_addr(x, MB_READY + (gc & 1)), (uint32_t)((gc >> 1) & 1))) return;
+        if (!first && !wait_bar(x, bar_addr(x, MB_O), par ^ 1u)) return;
+        if (!wait_bar(x, bar_addr(x, MB_ST), par)) return;
+        const uint64_t dk = kmaj_desc(a, 128, 0);
+        if (elect_one()) {
+            fence_after_sync();
+#pragma unroll 1
+            for (int t = 1; t >= 0; --t)
+#pragma unroll
+                for (int s = 0; s < D / 16; ++s)
+                    mma_bf16_tmem_a(tm + COL_PK, tm + COL_S + (uint32_t)(16 * s + 8 * t), dk + kstep(128, s), id_u,
+                                    t < 1 || s > 0);
+            mma_commit(mb);
+        }
+        __syncwarp();
+        is.ph ^= 1u;
+        // Pq^T = S^T Q^T
+        if (!wait_bar(x, bar_addr(x, MB_OT), par)) return;
+        if (elect_one()) {
+            fence_after_sync();
+#pragma unroll 1
+            for (int t = 1; t >= 0; --t)
+#pragma unroll
+                for (int s = 0; s < D / 16; ++s)
+                    mma_bf16_tmem_a(tm + COL_PQ, tm + COL_S + (uint32_t)(16 * s + 8 * t), dk + 512 + kstep(128, s), id_u,
+                                    t < 1 || s > 0);
+        }
+        __syncwarp();
+        // U^T = R^T (T Diag(beta))^T
+        if (!wait_bar(x, bar_addr(x, MB_RT), par)) return;
+        if (elect_one()) {
+            fence_after_sync();
+            const uint64_t dt = kmaj_desc(tb, 64, 0);
+            // terms (2,0), (1,1), (0,2), (1,0), (0,1), (0,0) of R and T Diag(beta)
+#pragma unroll 1
+            for (int t = 0; t < 6; ++t) {
+                const uint32_t ra = (0x001012u >> (4 * t)) & 3u, ta = (0x010210u >> (4 * t)) & 3u;
+#pragma unroll
+                for (int s = 0; s < C / 16; ++s)
+                    mma_bf16_tmem_a(tm + COL_PK, tm + COL_R + 32u * ra + 8u * s, dt + ta * 512u + kstep(64, s), id_u,
+                                    t > 0 || s > 0);
+            }
+            mma_commit(mb);
+            mma_commit(mt);
+        }
+        __syncwarp();
+        is.ph ^= 1u;
+        load_v();                          // every state warp has read this chunk's
+        // dS^T = U'^T K, then U^T B^T
+        if (!wait_bar(x, bar_addr(x, MB_UT), par)) return;
+        if (elect_one()) {
+            fence_after_sync();
+            const uint64_t dm = mn_desc(a, 16384, 0), da = kmaj_desc(aq, 64, 0);
+#pragma unroll 1
+            for (int t = 2; t >= 0; --t)
+#pragma unroll
+                for (int s = 0; s < C / 16; ++s)
+                    mma_bf16_tmem_a(tm + COL_S, tm + COL_R + 32u * t + 8u * s, dm + mnstep(s), id_s, t < 2 || s > 0);
+            mma_commit(mb);
+            // terms (1,0), (0,1), (0,0) of U and B
+#pragma unroll 1
+            for (int t = 0; t < 3; ++t) {
+                const uint32_t ua = t == 0, ba = t == 1;
+#pragma unroll
+                for (int s = 0; s < C / 16; ++s)
+                    mma_bf16_tmem_a(tm + COL_BU, tm + COL_PK + 16u * s + 8u * ua, da + ba * 512u + kstep(64, s), id_u,
+                                    t > 0 || s > 0);
+            }
+            mma_commit(mo);
+        }
+        __syncwarp();
+        if (left > 0) {
+            --left;
+            if (!issue_kk(x, is)) return;
+        }
+        // dS is done: so are all readers of this chunk's K and Q
+        if (!wait_bar(x, bar_addr(x, MB_S), is.ph)) return;
+        is.ph ^= 1u;
+        load_kq();
+    }
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -805,12 +1028,12 @@ packed_chunk_kernel(const __grid_constant__ PackedTcParams tp) {
         tmem_relinquish();
     }
     if (tid == 0) {
-        for (int i = 0; i < kNumBars; ++i) mbar_init(bar_addr(x, i), i == MB_DRAIN ? 2 : 1);
+        for (int i = 0; i < kNumBars; ++i) mbar_init(bar_addr(x, i), bar_count(i));
         *x.abort_flag = 0;
         fence_mbar_init();
     }
     // what lies above the diagonal of T Diag(beta) and B is never written again
-    for (uint32_t i = tid; i < (OFF_AKK - OFF_TB) / 16; i += kThreads)
+    for (uint32_t i = tid; i < (OFF_A - OFF_TB) / 16; i += kThreads)
         *reinterpret_cast<uint4 *>(sm + OFF_TB + 16 * i) = make_uint4(0, 0, 0, 0);
     fence_async_smem();
     fence_before_sync();
@@ -819,26 +1042,46 @@ packed_chunk_kernel(const __grid_constant__ PackedTcParams tp) {
     x.tm = *tmem_slot;
 
     const Sched sc = sched_of(sm);
-    int gc = 0, requested = 0;             // chunks of this CTA so far: stages and phases go on over pages
-    uint32_t ph = 0;
-    for (int s0 = 0; s0 < p.N; s0 += kPage) {
-        fill_page(p, sc, s0, tid);
-        if (warp < kStateThreads / 32) state_page(p, tp.tm, x, sc, s0, tid, gc, ph, requested);
-        else prep_page(p, x, sc, tid - kStateThreads, gc);
-        __syncthreads();
-        if (*x.abort_flag) break;
-    }
-
-    // TMEM is freed once every MMA issued is complete, and shared memory is left
-    // once every load requested has landed, after an abort too (bounded).
-    if (tid == 0 || tid == kStateThreads) {
-        mma_commit(bar_addr(x, MB_DRAIN));
-        for (uint32_t i = 0; i < kWaitTries; ++i)
-            if (mbar_try_wait_suspend(bar_addr(x, MB_DRAIN), 0u, kSuspendNs)) break;
-        for (int r = requested - 1; r >= 0 && r >= requested - 2; --r)
-            for (int b : {MB_KQ, MB_V})
-                for (uint32_t i = 0; i < kWaitTries; ++i)
-                    if (mbar_try_wait_suspend(bar_addr(x, b + (r & 1)), (uint32_t)((r >> 1) & 1), kSuspendNs)) break;
+    int gc = 0;                            // chunks of this CTA so far: stages and phases go on over pages
+    Issue is = {0, 0, 0, 0u};
+    if (warp < kStateWarps) {
+        regs_up<kStateRegs>();
+        uint32_t ph = 0;
+        for (int s0 = 0; s0 < p.N; s0 += kPage) {
+            fill_page(p, sc, s0, tid);
+            state_page(p, x, sc, s0, tid, gc, ph);
+            __syncthreads();
+            if (*x.abort_flag) break;
+        }
+    } else if (tid < kStateThreads + kPrepThreads) {
+        regs_down<kPrepRegs>();
+        for (int s0 = 0; s0 < p.N; s0 += kPage) {
+            fill_page(p, sc, s0, tid);
+            prep_page(p, x, sc, (tid - kStateThreads) / kGroup, (tid - kStateThreads) % kGroup, gc);
+            __syncthreads();
+            if (*x.abort_flag) break;
+        }
+    } else {                               // of these four warps one issues
+        regs_down<kIssueRegs>();
+        const bool issuer = warp == (kStateThreads + kPrepThreads) / 32;
+        for (int s0 = 0; s0 < p.N; s0 += kPage) {
+            fill_page(p, sc, s0, tid);
+            if (issuer) issue_page(p, tp.tm, x, sc, gc, is);
+            __syncthreads();
+            if (*x.abort_flag) break;
+        }
+        // TMEM is freed once every MMA issued is complete, and shared memory is left
+        // once every load requested has landed, after an abort too (bounded).
+        const uint32_t mb = uniform(bar_addr(x, MB_DRAIN));
+        if (issuer && elect_one()) mma_commit(mb);
+        __syncwarp();
+        auto done = [&](int bar, int phase) {
+            for (uint32_t i = 0; i < kWaitTries; ++i)
+                if (mbar_try_wait_suspend(bar_addr(x, bar), (uint32_t)(phase & 1), kSuspendNs)) break;
+        };
+        if (issuer) done(MB_DRAIN, 0);
+        for (int n = is.kq_n - 1; n >= 0 && n >= is.kq_n - kStages; --n) done(MB_KQ + n % kStages, n / kStages);
+        if (is.v_n > 0) done(MB_V, is.v_n - 1);
     }
     fence_before_sync();
     __syncthreads();

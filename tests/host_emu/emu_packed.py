@@ -35,6 +35,12 @@ inline float __shfl_up_sync(unsigned m, float v, int off) {
     return emu_lane_value(m, v, lane >= off ? lane - off : lane);
 }
 inline float __shfl_sync(unsigned m, float v, int src) { return emu_lane_value(m, v, src); }
+inline unsigned __byte_perm(unsigned a, unsigned b, unsigned s) {
+    const unsigned long long v = ((unsigned long long)b << 32) | a;
+    unsigned r = 0;
+    for (int i = 0; i < 4; ++i) r |= (unsigned)((v >> (8 * ((s >> (4 * i)) & 7))) & 0xFF) << (8 * i);
+    return r;
+}
 using std::memcpy;
 '''
 
