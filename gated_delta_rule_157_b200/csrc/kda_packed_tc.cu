@@ -75,18 +75,20 @@ constexpr uint32_t SMEM_USED = OFF_MISC + 256;
 constexpr uint32_t SMEM_BYTES = SMEM_USED + 1024;                // the base is rounded up to 1024
 static_assert(SMEM_BYTES <= 232448, "shared memory of one CTA");
 
-// Barriers.  KQ, V: loads landed.  READY: prep of a chunk done; FREE: its B and
-// row factors used; TBFREE: its T used.  KK: [K ; Q] K^T done; KKFREE: read.
-// S: P, U, dS done, in turn; O: O done.  From the state warps, one arrival each:
-// ST terms of S written, OT the O before taken, RT terms of R, UT of U and U'.
+// Barriers.  KQ, V: loads landed.  GATE: gates of a chunk written, GFREE: the
+// prep group done with them; READY: prep of a chunk done;
+// FREE: its B and row factors used; TBFREE: its T used.  KK: [K ; Q] K^T done;
+// KKFREE: read.  S: P, U, dS done, in turn; Q: Pq done; O: O done.  From the state
+// warps, one arrival each: ST terms of S written, RT of R, UT of U and U'; OT the
+// O before taken.
 enum {
     MB_KQ = 0, MB_V = 3, MB_READY = 4, MB_FREE = 6, MB_KK = 9, MB_KKFREE = 11, MB_TBFREE = 12, MB_S = 13, MB_O = 14,
-    MB_ST = 15, MB_OT = 16, MB_RT = 17, MB_UT = 18, MB_DRAIN = 19, kNumBars = 20
+    MB_ST = 15, MB_OT = 16, MB_RT = 17, MB_UT = 18, MB_DRAIN = 19, MB_GATE = 20, MB_GFREE = 22, MB_Q = 24, kNumBars = 25
 };
 __device__ __forceinline__ uint32_t bar_count(int i) {
     return (i >= MB_FREE && i < MB_KK) || (i >= MB_ST && i <= MB_UT) ? (uint32_t)kStateWarps : 1u;
 }
-constexpr uint32_t MISC_ABORT = 160, MISC_TMEM = 164, MISC_COUNT = 168;
+constexpr uint32_t MISC_ABORT = 208, MISC_TMEM = 212, MISC_COUNT = 216;
 
 // TMEM columns.  16 columns of an fp32 row become 8 + 8 columns of its two terms.
 constexpr uint32_t COL_S = 0;              // S^T: term t of k-step s at 16 s + 8 t; dS
@@ -346,31 +348,46 @@ __device__ __forceinline__ void request_v(const PackedParams &p, const CUtensorM
 __device__ __forceinline__ uint32_t tile_off(int r, int i) {      // 64 x 64 bf16, K-major, swizzled
     return (uint32_t)(r * 128 + (((i >> 3) ^ (r & 7)) << 4) + (i & 7) * 2);
 }
-// D (16 x 8) += A (16 x 8 KS) B (8 KS x 8), fp32 tiles in shared memory, each
+// D (16 x 8 NB) = A (16 x 16) B (16 x 8 NB), fp32 tiles in shared memory, each
 // operand as tf32 head and tail: three products, the error of an fp32 product.
-template <int KS>
-__device__ __forceinline__ void warp_mm(float d[4], const float *A, const float *B, int lane) {
+// Head times head and the cross terms run as chains of their own.
+template <int NB>
+__device__ __forceinline__ void warp_block(float (&d)[NB][4], const float *A, const float *B, int lane) {
     const int g = lane >> 2, t = lane & 3;
+    float e[NB][4];
 #pragma unroll
-    for (int kk = 0; kk < KS; ++kk) {
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e[n][i] = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
         const float *a = A + g * LDA + 8 * kk + t;
-        const float *b = B + (8 * kk + t) * LDA + g;
-        const float av[4] = {a[0], a[8 * LDA], a[4], a[8 * LDA + 4]}, bv[2] = {b[0], b[4 * LDA]};
-        uint32_t ah[4], al[4], bh[2], bl[2];
+        const float av[4] = {a[0], a[8 * LDA], a[4], a[8 * LDA + 4]};
+        uint32_t ah[4], al[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             ah[i] = to_tf32(av[i]);
             al[i] = to_tf32(av[i] - __uint_as_float(ah[i]));
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            bh[i] = to_tf32(bv[i]);
-            bl[i] = to_tf32(bv[i] - __uint_as_float(bh[i]));
+        for (int n = 0; n < NB; ++n) {
+            const float *b = B + (8 * kk + t) * LDA + 8 * n + g;
+            const float bv[2] = {b[0], b[4 * LDA]};
+            uint32_t bh[2], bl[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                bh[i] = to_tf32(bv[i]);
+                bl[i] = to_tf32(bv[i] - __uint_as_float(bh[i]));
+            }
+            mma_tf32_16x8x8(e[n], al, bh);
+            mma_tf32_16x8x8(d[n], ah, bh);
+            mma_tf32_16x8x8(e[n], ah, bl);
         }
-        mma_tf32_16x8x8(d, al, bh);
-        mma_tf32_16x8x8(d, ah, bl);
-        mma_tf32_16x8x8(d, ah, bh);
     }
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[n][i] += e[n][i];
 }
 __device__ __forceinline__ void warp_put(float *Dst, const float d[4], float sgn, bool accumulate, int lane) {
     const int g = lane >> 2, t = lane & 3;
@@ -384,17 +401,15 @@ __device__ __forceinline__ void warp_put(float *Dst, const float d[4], float sgn
     *p0 = v0;
     *p1 = v1;
 }
-// Gates of a chunk by one warp: lane = tokens lane, lane + 32.  Requested a
-// chunk of the group ahead and kept as loaded (a conversion would wait).
+// One chunk's gate inputs for the tokens lane, lane + 32, kept as loaded (a
+// conversion would wait for them).
 struct Gate {
     __nv_bfloat16 z[2], b[2];
     float A, bias;
-    int count;                             // rows of the chunk
     __device__ __forceinline__ void load(const PackedParams &p, const Sched &sc, const Cursor &c, int lane) {
-        count = c.valid() ? c.rows() : 0;
         A = bias = 0.f;
-        if (count == 0) return;
-        const int hv = c.head(p), row0 = sc.begin[c.seq(p, sc)] + c.n * C;
+        if (!c.valid()) return;
+        const int count = c.rows(), hv = c.head(p), row0 = sc.begin[c.seq(p, sc)] + c.n * C;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int t = lane + 32 * u;
@@ -409,52 +424,81 @@ struct Gate {
             if (p.dt_bias) bias = p.dt_bias[hv];
         }
     }
-    // Log-decays in log2 units, their running sum as head + tail, and beta.
-    __device__ __forceinline__ void store(const PackedParams &p, int lane, float *gh, float *gl, float *beta) const {
-        const float ea = p.gate_in ? expf(A) : 0.f;
-        float h[2], l[2];
+};
+// (ah, al) += (bh, bl), head and tail
+__device__ __forceinline__ void add_two(float &ah, float &al, float bh, float bl) {
+    const float s = ah + bh, v = s - ah;
+    const float e = (ah - (s - v)) + (bh - v) + al + bl;
+    ah = s + e;
+    al = e - (ah - s);
+}
+__device__ __forceinline__ float *group_vectors(uint8_t *sm, int grp) {       // G head, G tail, beta, rk, rq
+    return reinterpret_cast<float *>(sm + OFF_PREP + (uint32_t)grp * PREP_BYTES);
+}
+
+// =====================================================================
+// Gate warps, one per prep group: log-decays of a chunk in log2 units, their
+// running sum as head + tail, and beta, written when the group is done with
+// those of its last chunk.
+// =====================================================================
+__device__ __forceinline__ void gate_page(const PackedParams &p, const Ctx &x, const Sched &sc, int grp, int lane, int &gc) {
+    float *gh = group_vectors(x.sm, grp), *gl = gh + 64, *beta = gl + 64;
+    Cursor cur;
+    cur.start(p, sc);
+    if ((gc & 1) != grp && cur.valid()) {  // the other group's chunk
+        cur.next(p, sc);
+        ++gc;
+    }
+    Gate gate;
+    gate.load(p, sc, cur, lane);
+    while (cur.valid()) {
+        const int mine = gc, Cc = cur.rows();
+        const float ea = p.gate_in ? expf(gate.A) : 0.f;
+        float h[2], l[2] = {0.f, 0.f}, be[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int t = lane + 32 * u;
-            const float zu = __bfloat162float(z[u]), bu = __bfloat162float(b[u]);
-            float g = p.gate_in ? kda_gate(p.gate_in, zu, bias, ea, p.g_min) : zu;
+            const float zu = __bfloat162float(gate.z[u]), bu = __bfloat162float(gate.b[u]);
+            float g = p.gate_in ? kda_gate(p.gate_in, zu, gate.bias, ea, p.g_min) : zu;
             g *= kLog2E;
             // below 2^-150 a factor is 0 in fp32: a floor keeps the sums finite
             g = g < -1e4f ? -1e4f : g;
-            g = t < count ? g : 0.f;
-            h[u] = g;
-            beta[t] = t < count ? (p.beta_sigmoid ? sigmoidf_(bu) : bu) : 0.f;
+            h[u] = t < Cc ? g : 0.f;
+            be[u] = t < Cc ? (p.beta_sigmoid ? sigmoidf_(bu) : bu) : 0.f;
         }
-        l[0] = l[1] = 0.f;
-        auto add = [](float &ah, float &al, float bh, float bl) {     // (ah, al) += (bh, bl)
-            const float s = ah + bh, v = s - ah;
-            const float e = (ah - (s - v)) + (bh - v) + al + bl;
-            ah = s + e;
-            al = e - (ah - s);
-        };
+        cur.next(p, sc);                   // the group's next chunk is two on
+        ++gc;
+        if (cur.valid()) {
+            cur.next(p, sc);
+            ++gc;
+        }
+        gate.load(p, sc, cur, lane);
 #pragma unroll 1
         for (int off = 1; off < 32; off <<= 1) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const float oh = __shfl_up_sync(0xffffffffu, h[u], off), ol = __shfl_up_sync(0xffffffffu, l[u], off);
-                if (lane >= off) add(h[u], l[u], oh, ol);
+                if (lane >= off) add_two(h[u], l[u], oh, ol);
             }
         }
-        const float th = __shfl_sync(0xffffffffu, h[0], 31), tl = __shfl_sync(0xffffffffu, l[0], 31);
-        add(h[1], l[1], th, tl);
+        add_two(h[1], l[1], __shfl_sync(0xffffffffu, h[0], 31), __shfl_sync(0xffffffffu, l[0], 31));
+        if (mine >= 2 && !wait_bar(x, bar_addr(x, MB_GFREE + grp), (uint32_t)(((mine >> 1) - 1) & 1))) return;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             gh[lane + 32 * u] = h[u];
             gl[lane + 32 * u] = l[u];
+            beta[lane + 32 * u] = be[u];
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_addr(x, MB_GATE + grp));
     }
-};
+}
 
 __device__ __forceinline__ void prep_page(const PackedParams &p, const Ctx &x, const Sched &sc, int grp, int tid, int &gc) {
     uint8_t *sm = x.sm;
     const int lane = tid & 31, warp = tid >> 5, bar = BAR_PREP + grp;
-    float *gh = reinterpret_cast<float *>(sm + OFF_PREP + (uint32_t)grp * PREP_BYTES);
-    float *gl = gh + 64, *beta = gl + 64, *rk = beta + 64, *rq = rk + 64;
+    const float *gh = group_vectors(sm, grp), *gl = gh + 64, *beta = gl + 64;
+    float *rk = group_vectors(sm, grp) + 192, *rq = rk + 64;
     float *Am = reinterpret_cast<float *>(sm + OFF_A + (uint32_t)grp * A_BYTES);
     uint8_t *tb = sm + OFF_TB;
 
@@ -464,45 +508,46 @@ __device__ __forceinline__ void prep_page(const PackedParams &p, const Ctx &x, c
         cur.next(p, sc);
         ++gc;
     }
-    Gate gate;
-    if (warp == 3) gate.load(p, sc, cur, lane);
     for (; cur.valid(); ++gc) {
         const int stage = gc % kStages, Cc = cur.rows();
-        const uint8_t *kq = sm + OFF_KQ + (uint32_t)stage * KQ_BYTES;
         uint8_t *aqk = sm + OFF_AQK + (uint32_t)stage * 2 * 8192;
         float *vec = reinterpret_cast<float *>(sm + OFF_VEC + (uint32_t)stage * VEC_BYTES);
-        // A wait that gives up leaves its thread running to the chunk's one vote,
-        // where all return together.
-        bool ok = gc < kStages || wait_bar(x, bar_addr(x, MB_FREE + stage), (uint32_t)((gc / kStages - 1) & 1));
-        if (warp == 3) gate.store(p, lane, gh, gl, beta);
         cur.next(p, sc);                   // two on: the group's next chunk
         int step = 1;
         if (cur.valid()) {
             cur.next(p, sc);
             step = 2;
         }
-        if (warp == 3) gate.load(p, sc, cur, lane);
+        // A wait that gives up leaves its thread running to the chunk's one vote,
+        // where all return together.
+        //
+        // A wait for a phase needs the phase before complete.  Of KQ that is the load of
+        // chunk gc - 3, which the issuing warp saw landed before FREE of gc - 5, and that
+        // these threads waited for two chunks ago; the first chunks wait for FREE here.
+        auto freed = [&]() { return wait_bar(x, bar_addr(x, MB_FREE + stage), (uint32_t)((gc / kStages - 1) & 1)); };
+        bool ok = gc < kStages || gc >= kStages + 2 || freed();
         if (ok) ok = wait_bar(x, bar_addr(x, MB_KQ + stage), (uint32_t)((gc / kStages) & 1));
         // Norms: thread = row of [K ; Q].
         float ss;
         {
-            float2 s = make_float2(0.f, 0.f);
+            const uint8_t *kq = sm + OFF_KQ + (uint32_t)stage * KQ_BYTES + tid * 128;
+            float2 s0 = make_float2(0.f, 0.f), s1 = s0;
             if (p.l2norm) {
 #pragma unroll 4
                 for (int j = 0; j < 16; ++j) {
-                    const uint4 w = *reinterpret_cast<const uint4 *>(kq + (j >> 3) * 16384 + tid * 128 +
-                                                                     (((j & 7) ^ (tid & 7)) << 4));
-                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 f = make_float2(bf_lo(u[i]), bf_hi(u[i]));
-                        s = __ffma2_rn(f, f, s);
-                    }
+                    const uint4 w = *reinterpret_cast<const uint4 *>(kq + (j >> 3) * 16384 + (((j & 7) ^ (tid & 7)) << 4));
+                    const float2 f0 = make_float2(bf_lo(w.x), bf_hi(w.x)), f1 = make_float2(bf_lo(w.y), bf_hi(w.y));
+                    const float2 f2 = make_float2(bf_lo(w.z), bf_hi(w.z)), f3 = make_float2(bf_lo(w.w), bf_hi(w.w));
+                    s0 = __ffma2_rn(f0, f0, s0);
+                    s1 = __ffma2_rn(f1, f1, s1);
+                    s0 = __ffma2_rn(f2, f2, s0);
+                    s1 = __ffma2_rn(f3, f3, s1);
                 }
             }
-            ss = s.x + s.y;
+            ss = (s0.x + s1.x) + (s0.y + s1.y);
         }
-        named_bar(bar, kGroup);            // the gates
+        if (ok) ok = wait_bar(x, bar_addr(x, MB_GATE + grp), (uint32_t)((gc >> 1) & 1));
+        if (ok && gc >= kStages + 2) ok = freed();
         {                                  // row factors (0 behind the sequence's end)
             const int t = tid & 63;
             const float r = t < Cc ? (p.l2norm ? rsqrtf(ss + p.l2_eps) : 1.f) : 0.f;
@@ -537,11 +582,19 @@ __device__ __forceinline__ void prep_page(const PackedParams &p, const Ctx &x, c
                     const float4 h4 = *reinterpret_cast<const float4 *>(gh + j0 + j);
                     const float4 l4 = *reinterpret_cast<const float4 *>(gl + j0 + j);
                     const float4 r4 = *reinterpret_cast<const float4 *>(rk + j0 + j);
-                    const float hh[4] = {h4.x, h4.y, h4.z, h4.w}, ll[4] = {l4.x, l4.y, l4.z, l4.w};
-                    const float rr[4] = {r4.x, r4.y, r4.z, r4.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        v[j + i] = j0 + j + i <= last ? v[j + i] * (f * rr[i]) * ex2f_((hi - hh[i]) + (lo - ll[i])) : 0.f;
+                    const float2 m = make_float2(-1.f, -1.f);
+                    const float2 d0 = __fadd2_rn(__ffma2_rn(make_float2(h4.x, h4.y), m, make_float2(hi, hi)),
+                                                 __ffma2_rn(make_float2(l4.x, l4.y), m, make_float2(lo, lo)));
+                    const float2 d1 = __fadd2_rn(__ffma2_rn(make_float2(h4.z, h4.w), m, make_float2(hi, hi)),
+                                                 __ffma2_rn(make_float2(l4.z, l4.w), m, make_float2(lo, lo)));
+                    const float2 w0 = __fmul2_rn(make_float2(v[j], v[j + 1]),
+                                                 __fmul2_rn(make_float2(r4.x, r4.y), make_float2(f, f)));
+                    const float2 w1 = __fmul2_rn(make_float2(v[j + 2], v[j + 3]),
+                                                 __fmul2_rn(make_float2(r4.z, r4.w), make_float2(f, f)));
+                    v[j] = j0 + j <= last ? w0.x * ex2f_(d0.x) : 0.f;
+                    v[j + 1] = j0 + j + 1 <= last ? w0.y * ex2f_(d0.y) : 0.f;
+                    v[j + 2] = j0 + j + 2 <= last ? w1.x * ex2f_(d1.x) : 0.f;
+                    v[j + 3] = j0 + j + 3 <= last ? w1.y * ex2f_(d1.y) : 0.f;
                 }
                 if (is_q) {
 #pragma unroll
@@ -606,38 +659,39 @@ __device__ __forceinline__ void prep_page(const PackedParams &p, const Ctx &x, c
             }
         }
         named_bar(bar, kGroup);
-#pragma unroll 1
-        for (int task = warp; task < 12; task += 4) {
-            const int blk = task >> 1, nh = (task & 1) * 8;
-            const int arow = blk == 0 ? 16 : blk == 1 ? 48 : (blk == 2 || blk == 4) ? 32 : 48;
-            const int kc = blk == 1 ? 32 : (blk == 2 || blk == 3) ? 16 : 0;
-            const int drow = blk == 1 ? 32 : (blk == 3 || blk == 5) ? 16 : 0;
-            const int dcol = blk == 0 ? 16 : (blk == 4 || blk == 5) ? 32 : 48;
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
-            warp_mm<2>(d, Am + arow * LDA + kc, Am + kc * LDA + kc + nh, lane);
-            warp_put(Am + drow * LDA + dcol + nh, d, 1.f, false, lane);
+        {                                  // (1): a whole product and half of one per warp
+            const int arow = warp == 0 ? 16 : warp == 2 ? 32 : 48, kc = warp < 2 ? 0 : 16;
+            float *to = Am + (warp & 1 ? 16 : 0) * LDA + (warp == 0 ? 16 : warp == 1 ? 32 : 48);
+            const int nh = 8 * (warp & 1);
+            float d[2][4] = {}, h[1][4] = {};
+            warp_block<2>(d, Am + arow * LDA + kc, Am + kc * LDA + kc, lane);
+            if (warp < 2) warp_block<1>(h, Am + 32 * LDA, Am + nh, lane);
+            else warp_block<1>(h, Am + 48 * LDA + 32, Am + 32 * LDA + 32 + nh, lane);
+            warp_put(to, d[0], 1.f, false, lane);
+            warp_put(to + 8, d[1], 1.f, false, lane);
+            warp_put(Am + (warp < 2 ? 32 : 32 * LDA + 48) + nh, h[0], 1.f, false, lane);
         }
         named_bar(bar, kGroup);
-#pragma unroll 1
-        for (int i = 0; i < 2; ++i) {      // warp = task, both halves of its columns
-            const int nh = 8 * i;
+        {                                  // (2)
             const int arow = warp == 0 ? 16 : warp == 1 ? 48 : 16 * (warp - 2);
             const int acol = warp == 0 ? 16 : 48;
             const int brow = warp == 1 ? 32 : 0, bcol = warp == 1 ? 48 : 16;
-            const int drow = warp == 0 ? 16 : warp == 1 ? 48 : 16 * (warp - 2);
-            const int dcol = warp == 0 ? 0 : 32;
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
-            warp_mm<2>(d, Am + arow * LDA + acol, Am + brow * LDA + bcol + nh, lane);
-            warp_put(Am + drow * LDA + dcol + nh, d, -1.f, warp >= 2, lane);
+            float *to = Am + arow * LDA + (warp == 0 ? 0 : 32);
+            float d[2][4] = {};
+            warp_block<2>(d, Am + arow * LDA + acol, Am + brow * LDA + bcol, lane);
+            warp_put(to, d[0], -1.f, warp >= 2, lane);
+            warp_put(to + 8, d[1], -1.f, warp >= 2, lane);
         }
         named_bar(bar, kGroup);
-#pragma unroll 1
-        for (int mt = 0; mt < 2; ++mt) {   // warp = columns 8 warp ..
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
-            const float *A = Am + (32 + 16 * mt) * LDA + 32, *B = Am + 32 + 8 * warp;
-            warp_mm<2>(d, A, B, lane);
-            if (mt == 1) warp_mm<2>(d, A + 16, B + 16 * LDA, lane);
-            warp_put(Am + (32 + 16 * mt) * LDA + 8 * warp, d, -1.f, false, lane);
+        {                                  // (3): warp = (block row, block column)
+            const int mt = warp & 1, cb = warp >> 1;
+            const float *A = Am + (32 + 16 * mt) * LDA + 32, *B = Am + 32 + 16 * cb;
+            float *to = Am + (32 + 16 * mt) * LDA + 16 * cb;
+            float d[2][4] = {};
+            warp_block<2>(d, A, B, lane);
+            if (mt == 1) warp_block<2>(d, A + 16, B + 16 * LDA, lane);
+            warp_put(to, d[0], -1.f, false, lane);
+            warp_put(to + 8, d[1], -1.f, false, lane);
         }
         if (ok && gc > 0) ok = wait_bar(x, bar_addr(x, MB_TBFREE), (uint32_t)((gc - 1) & 1));
         named_bar(bar, kGroup);
@@ -667,7 +721,10 @@ __device__ __forceinline__ void prep_page(const PackedParams &p, const Ctx &x, c
         }
         fence_async_smem();
         named_bar(bar, kGroup);
-        if (tid == 0 && ok) mbar_arrive(bar_addr(x, MB_READY + grp));
+        if (tid == 0 && ok) {
+            mbar_arrive(bar_addr(x, MB_READY + grp));
+            mbar_arrive(bar_addr(x, MB_GFREE + grp));
+        }
         gc += step - 1;
     }
 }
@@ -771,17 +828,6 @@ __device__ __forceinline__ void state_page(const PackedParams &p, const Ctx &x, 
     for (; cur.valid(); ++gc) {
         const int stage = gc % kStages, before = (gc + kStages - 1) % kStages;
         const float *vec = reinterpret_cast<const float *>(sm + OFF_VEC + (uint32_t)stage * VEC_BYTES) + 32 * hf;
-        if (!first) {                      // O of the chunk before
-            uint32_t o[16];
-            if (!wait_bar(x, bar_addr(x, MB_O), (uint32_t)((gc - 1) & 1))) return;
-            fence_after_sync();
-            take_o(tl, hf, reinterpret_cast<const float *>(sm + OFF_VEC + (uint32_t)before * VEC_BYTES) + 64 + 32 * hf, o);
-            warp_arrive(x, MB_OT, lane);
-            if (lane == 0) mbar_arrive(bar_addr(x, MB_FREE + before));
-            store_o(p, o_at, o_count, lane, o);
-        } else {
-            warp_arrive(x, MB_OT, lane);
-        }
         if (!wait_bar(x, bar_addr(x, MB_READY + (gc & 1)), (uint32_t)((gc >> 1) & 1))) return;
         if (!wait_bar(x, bar_addr(x, MB_V), (uint32_t)(gc & 1))) return;
         if (!wait_bar(x, bar_addr(x, MB_S), ph)) return;
@@ -806,6 +852,21 @@ __device__ __forceinline__ void state_page(const PackedParams &p, const Ctx &x, 
             put_split<3>(tl + COL_R + (uint32_t)(16 * hf + 8 * q), 32, v);
         }
         warp_arrive(x, MB_RT, lane);
+        if (!first) {                      // meanwhile O of the chunk before
+            uint32_t o[16];
+            if (!wait_bar(x, bar_addr(x, MB_O), (uint32_t)((gc - 1) & 1))) return;
+            fence_after_sync();
+            take_o(tl, hf, reinterpret_cast<const float *>(sm + OFF_VEC + (uint32_t)before * VEC_BYTES) + 64 + 32 * hf, o);
+            fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bar_addr(x, MB_OT));
+                mbar_arrive(bar_addr(x, MB_FREE + before));
+            }
+            store_o(p, o_at, o_count, lane, o);
+        } else if (lane == 0) {
+            mbar_arrive(bar_addr(x, MB_OT));
+        }
         if (!wait_bar(x, bar_addr(x, MB_S), ph)) return;
         ph ^= 1u;
         fence_after_sync();
@@ -900,7 +961,7 @@ __device__ __forceinline__ void issue_page(const PackedParams &p, const CUtensor
                                            int &gc, Issue &is) {
     const uint32_t id_u = idesc_bf16(128, 64), id_s = idesc_bf16(128, 128, false, /*b_mn_major=*/true);
     const uint32_t tm = uniform(x.tm), mb = uniform(bar_addr(x, MB_S)), mo = uniform(bar_addr(x, MB_O));
-    const uint32_t mt = uniform(bar_addr(x, MB_TBFREE)), tb = uniform(x.sbase + OFF_TB);
+    const uint32_t mt = uniform(bar_addr(x, MB_TBFREE)), mq = uniform(bar_addr(x, MB_Q)), tb = uniform(x.sbase + OFF_TB);
     Cursor cur, kq, v;                     // the chunk at hand, the next K and Q, the next V to load
     cur.start(p, sc);
     if (!cur.valid()) return;
@@ -946,18 +1007,6 @@ __device__ __forceinline__ void issue_page(const PackedParams &p, const CUtensor
         }
         __syncwarp();
         is.ph ^= 1u;
-        // Pq^T = S^T Q^T
-        if (!wait_bar(x, bar_addr(x, MB_OT), par)) return;
-        if (elect_one()) {
-            fence_after_sync();
-#pragma unroll 1
-            for (int t = 1; t >= 0; --t)
-#pragma unroll
-                for (int s = 0; s < D / 16; ++s)
-                    mma_bf16_tmem_a(tm + COL_PQ, tm + COL_S + (uint32_t)(16 * s + 8 * t), dk + 512 + kstep(128, s), id_u,
-                                    t < 1 || s > 0);
-        }
-        __syncwarp();
         // U^T = R^T (T Diag(beta))^T
         if (!wait_bar(x, bar_addr(x, MB_RT), par)) return;
         if (elect_one()) {
@@ -978,8 +1027,22 @@ __device__ __forceinline__ void issue_page(const PackedParams &p, const CUtensor
         __syncwarp();
         is.ph ^= 1u;
         load_v();                          // every state warp has read this chunk's
-        // dS^T = U'^T K, then U^T B^T
+        // Pq^T = S^T Q^T, while the state warps split U
+        if (!wait_bar(x, bar_addr(x, MB_OT), par)) return;
+        if (elect_one()) {
+            fence_after_sync();
+#pragma unroll 1
+            for (int t = 1; t >= 0; --t)
+#pragma unroll
+                for (int s = 0; s < D / 16; ++s)
+                    mma_bf16_tmem_a(tm + COL_PQ, tm + COL_S + (uint32_t)(16 * s + 8 * t), dk + 512 + kstep(128, s), id_u,
+                                    t < 1 || s > 0);
+            mma_commit(mq);
+        }
+        __syncwarp();
+        // dS^T = U'^T K over the columns of S, then U^T B^T
         if (!wait_bar(x, bar_addr(x, MB_UT), par)) return;
+        if (!wait_bar(x, bar_addr(x, MB_Q), par)) return;
         if (elect_one()) {
             fence_after_sync();
             const uint64_t dm = mn_desc(a, 16384, 0), da = kmaj_desc(aq, 64, 0);
@@ -1061,12 +1124,14 @@ packed_chunk_kernel(const __grid_constant__ PackedTcParams tp) {
             __syncthreads();
             if (*x.abort_flag) break;
         }
-    } else {                               // of these four warps one issues
+    } else {                               // one warp issues, one serves each prep group, one has nothing to do
         regs_down<kIssueRegs>();
-        const bool issuer = warp == (kStateThreads + kPrepThreads) / 32;
+        const int w = warp - (kStateThreads + kPrepThreads) / 32;
+        const bool issuer = w == 0;
         for (int s0 = 0; s0 < p.N; s0 += kPage) {
             fill_page(p, sc, s0, tid);
             if (issuer) issue_page(p, tp.tm, x, sc, gc, is);
+            else if (w < 3) gate_page(p, x, sc, w - 1, tid & 31, gc);
             __syncthreads();
             if (*x.abort_flag) break;
         }
