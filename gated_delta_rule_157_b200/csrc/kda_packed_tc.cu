@@ -52,6 +52,7 @@ using namespace tc;
 constexpr int C = 64, D = 128;
 constexpr int kStateThreads = 256, kPrepThreads = 256, kThreads = kStateThreads + kPrepThreads + 128;
 constexpr int kStateWarps = kStateThreads / 32;
+constexpr int kFirstState = 128, kFirstPrep = kFirstState + kStateThreads;     // threads below: the issuing warpgroup
 constexpr int kGroup = 128;                // threads of a prep group
 constexpr int LDA = 68;                    // row of the fp32 solve tiles
 constexpr int kPage = 128;                 // sequences scheduled at a time
@@ -82,13 +83,13 @@ static_assert(SMEM_BYTES <= 232448, "shared memory of one CTA");
 // warps, one arrival each: ST terms of S written, RT of R, UT of U and U'; OT the
 // O before taken.
 enum {
-    MB_KQ = 0, MB_V = 3, MB_READY = 4, MB_FREE = 6, MB_KK = 9, MB_KKFREE = 11, MB_TBFREE = 12, MB_S = 13, MB_O = 14,
-    MB_ST = 15, MB_OT = 16, MB_RT = 17, MB_UT = 18, MB_DRAIN = 19, MB_GATE = 20, MB_GFREE = 22, MB_Q = 24, kNumBars = 25
+    MB_KQ = 0, MB_V = 3, MB_READY = 4, MB_FREE = 6, MB_KK = 9, MB_KKFREE = 11, MB_S = 13, MB_O = 14,
+    MB_ST = 15, MB_OT = 16, MB_RT = 17, MB_UT = 18, MB_DRAIN = 19, MB_GATE = 20, MB_GFREE = 22, MB_TBFREE = 24, MB_Q = 26, kNumBars = 27
 };
 __device__ __forceinline__ uint32_t bar_count(int i) {
     return (i >= MB_FREE && i < MB_KK) || (i >= MB_ST && i <= MB_UT) ? (uint32_t)kStateWarps : 1u;
 }
-constexpr uint32_t MISC_ABORT = 208, MISC_TMEM = 212, MISC_COUNT = 216;
+constexpr uint32_t MISC_ABORT = 224, MISC_TMEM = 228, MISC_COUNT = 232;
 
 // TMEM columns.  16 columns of an fp32 row become 8 + 8 columns of its two terms.
 constexpr uint32_t COL_S = 0;              // S^T: term t of k-step s at 16 s + 8 t; dS
@@ -187,16 +188,19 @@ __device__ __forceinline__ void split2(float2 v, uint32_t (&w)[N]) {
 // col + stride, ...
 template <int N>
 __device__ __forceinline__ void put_split(uint32_t taddr, uint32_t stride, const float2 (&v)[8]) {
-    uint32_t w[N][8];
+    float2 r[8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-        uint32_t t[N];
-        split2<N>(v[u], t);
+    for (int u = 0; u < 8; ++u) r[u] = v[u];
 #pragma unroll
-        for (int i = 0; i < N; ++i) w[i][u] = t[i];
+    for (int i = 0; i < N; ++i) {          // term by term: eight words live at a time
+        uint32_t w[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            w[u] = pack_bf16x2(r[u].x, r[u].y);
+            if (i + 1 < N) r[u] = __ffma2_rn(make_float2(bf_lo(w[u]), bf_hi(w[u])), make_float2(-1.f, -1.f), r[u]);
+        }
+        tmem_st8(taddr + (uint32_t)i * stride, w);
     }
-#pragma unroll
-    for (int i = 0; i < N; ++i) tmem_st8(taddr + (uint32_t)i * stride, w[i]);
 }
 // The same as two terms over the 16 columns themselves.
 __device__ __forceinline__ void put_two(uint32_t taddr, const float2 (&v)[8]) { put_split<2>(taddr, 8, v); }
@@ -343,7 +347,7 @@ __device__ __forceinline__ void request_v(const PackedParams &p, const CUtensorM
 }
 
 // =====================================================================
-// Prep role: warps 8-11 the even chunks, warps 12-15 the odd ones.
+// Prep role: one group of four warps for the even chunks, one for the odd.
 // =====================================================================
 __device__ __forceinline__ uint32_t tile_off(int r, int i) {      // 64 x 64 bf16, K-major, swizzled
     return (uint32_t)(r * 128 + (((i >> 3) ^ (r & 7)) << 4) + (i & 7) * 2);
@@ -693,7 +697,8 @@ __device__ __forceinline__ void prep_page(const PackedParams &p, const Ctx &x, c
             warp_put(to, d[0], -1.f, false, lane);
             warp_put(to + 8, d[1], -1.f, false, lane);
         }
-        if (ok && gc > 0) ok = wait_bar(x, bar_addr(x, MB_TBFREE), (uint32_t)((gc - 1) & 1));
+        // (of chunk gc - 1; a barrier per parity, whose phase before is chunk gc - 3's)
+        if (ok && gc > 0) ok = wait_bar(x, bar_addr(x, MB_TBFREE + ((gc - 1) & 1)), (uint32_t)(((gc - 1) >> 1) & 1));
         named_bar(bar, kGroup);
         {                                  // T Diag(beta) as three terms: warp = block row, lane pair = row
             const int r = tid >> 1;
@@ -730,7 +735,7 @@ __device__ __forceinline__ void prep_page(const PackedParams &p, const Ctx &x, c
 }
 
 // =====================================================================
-// State role: warps 0-7.  Thread = (TMEM lane = value channel j, half hf).
+// State role.  Thread = (TMEM lane = value channel j, half hf).
 // =====================================================================
 // One chain's S and where its outputs go.
 struct Chain {
@@ -810,7 +815,7 @@ __device__ __forceinline__ void state_page(const PackedParams &p, const Ctx &x, 
                                            uint32_t &ph) {
     uint8_t *sm = x.sm;
     const int warp = tid >> 5, lane = tid & 31, hf = warp >> 2, j = (warp & 3) * 32 + lane;
-    const uint32_t tl = x.tm + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t tl = x.tm + ((uint32_t)((warp & 3) * 32) << 16);    // (roles begin at multiples of four warps)
 
     Cursor cur;
     cur.start(p, sc);
@@ -828,6 +833,16 @@ __device__ __forceinline__ void state_page(const PackedParams &p, const Ctx &x, 
     for (; cur.valid(); ++gc) {
         const int stage = gc % kStages, before = (gc + kStages - 1) % kStages;
         const float *vec = reinterpret_cast<const float *>(sm + OFF_VEC + (uint32_t)stage * VEC_BYTES) + 32 * hf;
+        uint32_t o[16];                    // O of the chunk before, until the wait for U
+        if (!first) {
+            if (!wait_bar(x, bar_addr(x, MB_O), (uint32_t)((gc - 1) & 1))) return;
+            fence_after_sync();
+            take_o(tl, hf, reinterpret_cast<const float *>(sm + OFF_VEC + (uint32_t)before * VEC_BYTES) + 64 + 32 * hf, o);
+            fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_addr(x, MB_FREE + before));
+        }
+        if (lane == 0) mbar_arrive(bar_addr(x, MB_OT));
         if (!wait_bar(x, bar_addr(x, MB_READY + (gc & 1)), (uint32_t)((gc >> 1) & 1))) return;
         if (!wait_bar(x, bar_addr(x, MB_V), (uint32_t)(gc & 1))) return;
         if (!wait_bar(x, bar_addr(x, MB_S), ph)) return;
@@ -852,21 +867,7 @@ __device__ __forceinline__ void state_page(const PackedParams &p, const Ctx &x, 
             put_split<3>(tl + COL_R + (uint32_t)(16 * hf + 8 * q), 32, v);
         }
         warp_arrive(x, MB_RT, lane);
-        if (!first) {                      // meanwhile O of the chunk before
-            uint32_t o[16];
-            if (!wait_bar(x, bar_addr(x, MB_O), (uint32_t)((gc - 1) & 1))) return;
-            fence_after_sync();
-            take_o(tl, hf, reinterpret_cast<const float *>(sm + OFF_VEC + (uint32_t)before * VEC_BYTES) + 64 + 32 * hf, o);
-            fence_before_sync();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(bar_addr(x, MB_OT));
-                mbar_arrive(bar_addr(x, MB_FREE + before));
-            }
-            store_o(p, o_at, o_count, lane, o);
-        } else if (lane == 0) {
-            mbar_arrive(bar_addr(x, MB_OT));
-        }
+        if (!first) store_o(p, o_at, o_count, lane, o);
         if (!wait_bar(x, bar_addr(x, MB_S), ph)) return;
         ph ^= 1u;
         fence_after_sync();
@@ -920,7 +921,7 @@ __device__ __forceinline__ void state_page(const PackedParams &p, const Ctx &x, 
     }
     if (!wait_bar(x, bar_addr(x, MB_O), (uint32_t)((gc - 1) & 1))) return;
     fence_after_sync();
-    uint32_t o[16];
+    uint32_t o[16];                        // the last chunk's
     take_o(tl, hf, reinterpret_cast<const float *>(sm + OFF_VEC + (uint32_t)((gc - 1) % kStages) * VEC_BYTES) + 64 + 32 * hf, o);
     fence_before_sync();
     __syncwarp();
@@ -930,8 +931,7 @@ __device__ __forceinline__ void state_page(const PackedParams &p, const Ctx &x, 
 
 // =====================================================================
 // Issuing warp: loads and MMAs, one elected lane, in the order the chunks need
-// them.  The product for the prep warps goes last in a chunk, where the tensor
-// pipe waits for the state warps.
+// them.
 // =====================================================================
 struct Issue {
     int kq_n, v_n, kk_n;                   // chunks of this CTA requested, and multiplied for the prep warps
@@ -1007,6 +1007,23 @@ __device__ __forceinline__ void issue_page(const PackedParams &p, const CUtensor
         }
         __syncwarp();
         is.ph ^= 1u;
+        // Pq^T = S^T Q^T and a product for the prep warps, while the state warps work on R
+        if (!wait_bar(x, bar_addr(x, MB_OT), par)) return;
+        if (elect_one()) {
+            fence_after_sync();
+#pragma unroll 1
+            for (int t = 1; t >= 0; --t)
+#pragma unroll
+                for (int s = 0; s < D / 16; ++s)
+                    mma_bf16_tmem_a(tm + COL_PQ, tm + COL_S + (uint32_t)(16 * s + 8 * t), dk + 512 + kstep(128, s), id_u,
+                                    t < 1 || s > 0);
+            mma_commit(mq);
+        }
+        __syncwarp();
+        if (left > 0) {
+            --left;
+            if (!issue_kk(x, is)) return;
+        }
         // U^T = R^T (T Diag(beta))^T
         if (!wait_bar(x, bar_addr(x, MB_RT), par)) return;
         if (elect_one()) {
@@ -1022,24 +1039,11 @@ __device__ __forceinline__ void issue_page(const PackedParams &p, const CUtensor
                                     t > 0 || s > 0);
             }
             mma_commit(mb);
-            mma_commit(mt);
+            mma_commit(mt + 8u * par);
         }
         __syncwarp();
         is.ph ^= 1u;
         load_v();                          // every state warp has read this chunk's
-        // Pq^T = S^T Q^T, while the state warps split U
-        if (!wait_bar(x, bar_addr(x, MB_OT), par)) return;
-        if (elect_one()) {
-            fence_after_sync();
-#pragma unroll 1
-            for (int t = 1; t >= 0; --t)
-#pragma unroll
-                for (int s = 0; s < D / 16; ++s)
-                    mma_bf16_tmem_a(tm + COL_PQ, tm + COL_S + (uint32_t)(16 * s + 8 * t), dk + 512 + kstep(128, s), id_u,
-                                    t < 1 || s > 0);
-            mma_commit(mq);
-        }
-        __syncwarp();
         // dS^T = U'^T K over the columns of S, then U^T B^T
         if (!wait_bar(x, bar_addr(x, MB_UT), par)) return;
         if (!wait_bar(x, bar_addr(x, MB_Q), par)) return;
@@ -1064,10 +1068,6 @@ __device__ __forceinline__ void issue_page(const PackedParams &p, const CUtensor
             mma_commit(mo);
         }
         __syncwarp();
-        if (left > 0) {
-            --left;
-            if (!issue_kk(x, is)) return;
-        }
         // dS is done: so are all readers of this chunk's K and Q
         if (!wait_bar(x, bar_addr(x, MB_S), is.ph)) return;
         is.ph ^= 1u;
@@ -1078,8 +1078,8 @@ __device__ __forceinline__ void issue_page(const PackedParams &p, const CUtensor
 __global__ void __launch_bounds__(kThreads, 1)
 packed_chunk_kernel(const __grid_constant__ PackedTcParams tp) {
     const PackedParams &p = tp.p;
-    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                              ~static_cast<uintptr_t>(1023));
+    // rounded up by an offset, not through an integer, so that accesses stay shared-memory ones
+    uint8_t *sm = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     const int tid = threadIdx.x, warp = tid >> 5;
     Ctx x;
     x.sm = sm;
@@ -1107,31 +1107,30 @@ packed_chunk_kernel(const __grid_constant__ PackedTcParams tp) {
     const Sched sc = sched_of(sm);
     int gc = 0;                            // chunks of this CTA so far: stages and phases go on over pages
     Issue is = {0, 0, 0, 0u};
-    if (warp < kStateWarps) {
+    if (tid >= kFirstState && tid < kFirstPrep) {
         regs_up<kStateRegs>();
         uint32_t ph = 0;
         for (int s0 = 0; s0 < p.N; s0 += kPage) {
             fill_page(p, sc, s0, tid);
-            state_page(p, x, sc, s0, tid, gc, ph);
+            state_page(p, x, sc, s0, tid - kFirstState, gc, ph);
             __syncthreads();
             if (*x.abort_flag) break;
         }
-    } else if (tid < kStateThreads + kPrepThreads) {
+    } else if (tid >= kFirstPrep) {
         regs_down<kPrepRegs>();
         for (int s0 = 0; s0 < p.N; s0 += kPage) {
             fill_page(p, sc, s0, tid);
-            prep_page(p, x, sc, (tid - kStateThreads) / kGroup, (tid - kStateThreads) % kGroup, gc);
+            prep_page(p, x, sc, (tid - kFirstPrep) / kGroup, (tid - kFirstPrep) % kGroup, gc);
             __syncthreads();
             if (*x.abort_flag) break;
         }
     } else {                               // one warp issues, one serves each prep group, one has nothing to do
         regs_down<kIssueRegs>();
-        const int w = warp - (kStateThreads + kPrepThreads) / 32;
-        const bool issuer = w == 0;
+        const bool issuer = warp == 0;     // the oldest warp, so that it is not kept waiting for a slot
         for (int s0 = 0; s0 < p.N; s0 += kPage) {
             fill_page(p, sc, s0, tid);
             if (issuer) issue_page(p, tp.tm, x, sc, gc, is);
-            else if (w < 3) gate_page(p, x, sc, w - 1, tid & 31, gc);
+            else if (warp < 3) gate_page(p, x, sc, warp - 1, tid & 31, gc);
             __syncthreads();
             if (*x.abort_flag) break;
         }
