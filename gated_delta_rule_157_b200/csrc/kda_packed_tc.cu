@@ -107,7 +107,7 @@ enum { BAR_PREP = 1 };                     // + group
 // to no more than the block is launched with (640 x 96: the kernel's launch
 // bounds leave 102, allocated in eights) -- an increase beyond that would wait
 // for ever.
-constexpr int kLaunchRegs = 96, kStateRegs = 136, kPrepRegs = 80, kIssueRegs = 48;
+constexpr int kLaunchRegs = 96, kStateRegs = 144, kPrepRegs = 72, kIssueRegs = 48;
 static_assert(kStateThreads * kStateRegs + kPrepThreads * kPrepRegs + 128 * kIssueRegs <= kThreads * kLaunchRegs,
               "register shares");
 template <int N>
@@ -833,16 +833,21 @@ __device__ __forceinline__ void state_page(const PackedParams &p, const Ctx &x, 
     for (; cur.valid(); ++gc) {
         const int stage = gc % kStages, before = (gc + kStages - 1) % kStages;
         const float *vec = reinterpret_cast<const float *>(sm + OFF_VEC + (uint32_t)stage * VEC_BYTES) + 32 * hf;
-        uint32_t o[16];                    // O of the chunk before, until the wait for U
-        if (!first) {
+        if (!first) {                      // O of the chunk before, while P is computed
+            uint32_t o[16];
             if (!wait_bar(x, bar_addr(x, MB_O), (uint32_t)((gc - 1) & 1))) return;
             fence_after_sync();
             take_o(tl, hf, reinterpret_cast<const float *>(sm + OFF_VEC + (uint32_t)before * VEC_BYTES) + 64 + 32 * hf, o);
             fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar_addr(x, MB_FREE + before));
+            if (lane == 0) {
+                mbar_arrive(bar_addr(x, MB_OT));
+                mbar_arrive(bar_addr(x, MB_FREE + before));
+            }
+            store_o(p, o_at, o_count, lane, o);
+        } else if (lane == 0) {
+            mbar_arrive(bar_addr(x, MB_OT));
         }
-        if (lane == 0) mbar_arrive(bar_addr(x, MB_OT));
         if (!wait_bar(x, bar_addr(x, MB_READY + (gc & 1)), (uint32_t)((gc >> 1) & 1))) return;
         if (!wait_bar(x, bar_addr(x, MB_V), (uint32_t)(gc & 1))) return;
         if (!wait_bar(x, bar_addr(x, MB_S), ph)) return;
@@ -867,7 +872,6 @@ __device__ __forceinline__ void state_page(const PackedParams &p, const Ctx &x, 
             put_split<3>(tl + COL_R + (uint32_t)(16 * hf + 8 * q), 32, v);
         }
         warp_arrive(x, MB_RT, lane);
-        if (!first) store_o(p, o_at, o_count, lane, o);
         if (!wait_bar(x, bar_addr(x, MB_S), ph)) return;
         ph ^= 1u;
         fence_after_sync();
