@@ -11,8 +11,11 @@
 // (row group, quad of columns); only the RG row groups meet, in log2(RG)
 // shuffle steps, and no warp waits for another inside a tile of tokens.  What
 // depends on the token alone (norms, gates, ka, qa) is prepared by the block
-// for a tile of two tokens per warp into a double shared buffer while the
-// previous tile is computed: one block barrier per tile.
+// for a tile of TPW tokens per warp.  Long sequences (LOOP) prepare two tokens
+// a warp into a double shared buffer, the next tile's rows requested while one is
+// computed: one block barrier per tile.  Where the caller knows that sequences fit
+// one tile of a token per warp (decode, verification) nothing is kept for a next tile, which
+// leaves registers for more blocks: there it is the traffic that counts.
 #include "kda_packed.cuh"
 
 namespace kda {
@@ -22,7 +25,6 @@ __device__ unsigned int g_packed_error = 0;
 
 constexpr int kRG = 8;                     // row groups (lanes along a column)
 constexpr int kCW = 4 * 32 / kRG;          // state columns per warp
-constexpr int kTPW = 2;                    // tokens a warp prepares per tile
 
 extern __shared__ float smem[];
 
@@ -55,7 +57,8 @@ struct TokenPrep {
         beta = ld_act(static_cast<const Tin *>(p.beta) + row * p.ldb, hv);
     }
 
-    __device__ __forceinline__ void store(const PackedParams &p, int hv, float ea, int lane, float *out) {
+    // `bias`: dt_bias of this lane's channels, 0 beyond them.
+    __device__ __forceinline__ void store(const PackedParams &p, const float (&bias)[NC], float ea, int lane, float *out) {
         float sq = 0.f, sk = 0.f, qk = 0.f;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
@@ -73,8 +76,7 @@ struct TokenPrep {
         const float rk = p.l2norm ? 1.f / sqrtf(sk + p.l2_eps) : 1.f;
         float a_head = 0.f;
         if (PER_HEAD) {
-            const float b = p.dt_bias && p.gate_in ? p.dt_bias[hv] : 0.f;
-            a_head = expf(p.gate_in ? kda_gate(p.gate_in, g[0], b, ea, p.g_min) : g[0]);
+            a_head = expf(p.gate_in ? kda_gate(p.gate_in, g[0], bias[0], ea, p.g_min) : g[0]);
         }
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
@@ -86,8 +88,7 @@ struct TokenPrep {
                 out[DKP + c] = qn;
             } else {
                 const bool in = c < p.Dk;
-                const float b = in && p.dt_bias && p.gate_in ? p.dt_bias[(size_t)hv * p.Dk + c] : 0.f;
-                const float a = in ? expf(p.gate_in ? kda_gate(p.gate_in, g[i], b, ea, p.g_min) : g[i]) : 0.f;
+                const float a = in ? expf(p.gate_in ? kda_gate(p.gate_in, g[i], bias[i], ea, p.g_min) : g[i]) : 0.f;
                 out[c] = kn * a;
                 out[DKP + c] = qn * a;
                 out[2 * DKP + c] = kn;
@@ -105,8 +106,8 @@ struct TokenPrep {
     }
 };
 
-template <typename Tin, int RPL, bool PER_HEAD>
-__global__ void __launch_bounds__(256)
+template <typename Tin, int RPL, bool PER_HEAD, int TPW, bool LOOP>
+__global__ void __launch_bounds__(256, LOOP ? 1 : 2)
 packed_recurrent_kernel(const PackedParams p) {
     constexpr int DKP = RPL * kRG;
     constexpr int TF = token_floats(DKP, PER_HEAD);
@@ -117,16 +118,32 @@ packed_recurrent_kernel(const PackedParams p) {
     const bool col_ok = col < p.Dv;
 
     const PackedSeq sq = packed_seq(p.cu, p.slots, p.T, p.P, s);
-    const bool repeat = __syncthreads_or(packed_repeat(p.slots, s, sq.slot, tid, blockDim.x));
-    if ((sq.bad || repeat) && tid == 0 && hv == 0 && blockIdx.y == 0) atomicOr(&g_packed_error, kPackedRange);
     // a sequence without rows changes nothing
-    if (sq.bad || repeat || sq.slot < 0 || sq.len == 0 || sq.len > p.split) return;
+    const bool mine = !sq.bad && sq.slot >= 0 && sq.len > 0 && sq.len <= p.split;
+
+    // The first rows before the state, so that they are prepared while it is on its way.
+    const int tile = TPW * warps;
+    TokenPrep<Tin, RPL, PER_HEAD> raw[TPW];
+#pragma unroll
+    for (int u = 0; u < TPW; ++u) {
+        const int t = warp * TPW + u;
+        if (mine && t < sq.len) raw[u].load(p, (long long)sq.begin + t, h, hv, lane);
+    }
+    constexpr int NC = TokenPrep<Tin, RPL, PER_HEAD>::NC;
+    const float A = p.gate_in ? p.A_log[hv] : 0.f;
+    float bias[NC];
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        const int c = lane + 32 * i;
+        bias[i] = 0.f;
+        if (p.gate_in && p.dt_bias && (PER_HEAD ? i == 0 : c < p.Dk)) bias[i] = p.dt_bias[PER_HEAD ? hv : (size_t)hv * p.Dk + c];
+    }
 
     // The state: rows (i / 4) * 4 RG + 4 rg + i % 4 of this lane's four columns,
     // kept as row pairs so that the prepared vectors feed packed FMAs directly.
-    float *S = p.pool + ((size_t)sq.slot * p.HV + hv) * p.Dk * p.Dv + col;
+    float *S = p.pool + ((size_t)(mine ? sq.slot : 0) * p.HV + hv) * p.Dk * p.Dv + col;
     float2 st[RPL / 2][4];
-    const bool zero = p.fresh && p.fresh[s];
+    const bool zero = !mine || (p.fresh && p.fresh[s]);
 #pragma unroll
     for (int i = 0; i < RPL; ++i) {
         const int r = (i >> 2) * (4 * kRG) + 4 * rg + (i & 3);
@@ -139,26 +156,24 @@ packed_recurrent_kernel(const PackedParams p) {
         }
     }
 
-    const float ea = p.gate_in ? expf(p.A_log[hv]) : 0.f;
-    const int tile = kTPW * warps;
-    TokenPrep<Tin, RPL, PER_HEAD> raw[kTPW];
-#pragma unroll
-    for (int u = 0; u < kTPW; ++u) {
-        const int t = warp * kTPW + u;
-        if (t < sq.len) raw[u].load(p, (long long)sq.begin + t, h, hv, lane);
-    }
+    const bool repeat = __syncthreads_or(packed_repeat(p.slots, s, sq.slot, tid, blockDim.x));
+    if ((sq.bad || repeat) && tid == 0 && hv == 0 && blockIdx.y == 0) atomicOr(&g_packed_error, kPackedRange);
+    if (!mine || repeat) return;
+    const float ea = expf(A);
     for (int t0 = 0, buf = 0; t0 < sq.len; t0 += tile, buf ^= 1) {
-        float *tok = smem + buf * tile * TF;
+        float *tok = smem + (LOOP ? buf * tile * TF : 0);
 #pragma unroll
-        for (int u = 0; u < kTPW; ++u) {
-            const int t = t0 + warp * kTPW + u;
-            if (t < sq.len) raw[u].store(p, hv, ea, lane, tok + (warp * kTPW + u) * TF);
+        for (int u = 0; u < TPW; ++u) {
+            const int t = t0 + warp * TPW + u;
+            if (t < sq.len) raw[u].store(p, bias, ea, lane, tok + (warp * TPW + u) * TF);
         }
         __syncthreads();
+        if (LOOP) {
 #pragma unroll
-        for (int u = 0; u < kTPW; ++u) {               // the next tile's rows, in flight meanwhile
-            const int t = t0 + tile + warp * kTPW + u;
-            if (t < sq.len) raw[u].load(p, (long long)sq.begin + t, h, hv, lane);
+            for (int u = 0; u < TPW; ++u) {            // the next tile's rows, in flight meanwhile
+                const int t = t0 + tile + warp * TPW + u;
+                if (t < sq.len) raw[u].load(p, (long long)sq.begin + t, h, hv, lane);
+            }
         }
         const int n = min(tile, sq.len - t0);
 #pragma unroll 1
@@ -223,6 +238,14 @@ packed_recurrent_kernel(const PackedParams p) {
                 }
             }
         }
+        if (!LOOP && t0 + tile < sq.len) { // a sequence longer than the caller said
+            __syncthreads();
+#pragma unroll
+            for (int u = 0; u < TPW; ++u) {
+                const int t = t0 + tile + warp * TPW + u;
+                if (t < sq.len) raw[u].load(p, (long long)sq.begin + t, h, hv, lane);
+            }
+        }
     }
 #pragma unroll
     for (int i = 0; i < RPL; ++i) {
@@ -236,32 +259,35 @@ packed_recurrent_kernel(const PackedParams p) {
     }
 }
 
-template <typename Tin, int RPL, bool PER_HEAD>
+template <typename Tin, int RPL, bool PER_HEAD, int TPW, bool LOOP>
 cudaError_t launch_one(const PackedParams &p, int warps, cudaStream_t s) {
     const int all = (p.Dv + kCW - 1) / kCW;
     const dim3 grid((unsigned)p.N * (unsigned)p.HV, (unsigned)((all + warps - 1) / warps));
-    const size_t bytes = (size_t)2 * kTPW * warps * token_floats(RPL * kRG, PER_HEAD) * sizeof(float);
-    auto kernel = packed_recurrent_kernel<Tin, RPL, PER_HEAD>;
+    const size_t bytes = (size_t)(LOOP ? 2 : 1) * TPW * warps * token_floats(RPL * kRG, PER_HEAD) * sizeof(float);
+    auto kernel = packed_recurrent_kernel<Tin, RPL, PER_HEAD, TPW, LOOP>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) return e;
     kernel<<<grid, 32 * warps, bytes, s>>>(p);
     return cudaGetLastError();
 }
 
+template <typename Tin, int RPL, bool PER_HEAD>
+cudaError_t launch_len(const PackedParams &p, int max_len, cudaStream_t s) {
+    const int all = (p.Dv + kCW - 1) / kCW;
+    if (max_len <= all) return launch_one<Tin, RPL, PER_HEAD, 1, false>(p, all, s);
+    return launch_one<Tin, RPL, PER_HEAD, 2, true>(p, all < 4 ? all : 4, s);
+}
+
 template <typename Tin>
-cudaError_t launch_type(const PackedParams &p, int warps, cudaStream_t s) {
-    if (p.Dk <= 64)
-        return p.g_per_head ? launch_one<Tin, 8, true>(p, warps, s) : launch_one<Tin, 8, false>(p, warps, s);
-    return p.g_per_head ? launch_one<Tin, 16, true>(p, warps, s) : launch_one<Tin, 16, false>(p, warps, s);
+cudaError_t launch_type(const PackedParams &p, int max_len, cudaStream_t s) {
+    if (p.Dk <= 64) return p.g_per_head ? launch_len<Tin, 8, true>(p, max_len, s) : launch_len<Tin, 8, false>(p, max_len, s);
+    return p.g_per_head ? launch_len<Tin, 16, true>(p, max_len, s) : launch_len<Tin, 16, false>(p, max_len, s);
 }
 
 }  // namespace
 
 cudaError_t launch_packed_recurrent(const PackedParams &p, bool bf16, int max_len, cudaStream_t s) {
-    (void)max_len;
-    const int all = (p.Dv + kCW - 1) / kCW;
-    const int warps = all < 4 ? all : 4;
-    return bf16 ? launch_type<__nv_bfloat16>(p, warps, s) : launch_type<float>(p, warps, s);
+    return bf16 ? launch_type<__nv_bfloat16>(p, max_len, s) : launch_type<float>(p, max_len, s);
 }
 
 cudaError_t read_and_clear_packed_error(unsigned int *out) {

@@ -46,18 +46,24 @@ using std::memcpy;
 
 _RUN_RECURRENT = _POISON + r'''
 extern "C" int emu_sizeof_packed_params(void) { return (int)sizeof(kda::PackedParams); }
-template <typename Tin, int RPL, bool PER_HEAD>
+template <typename Tin, int RPL, bool PER_HEAD, int TPW, bool LOOP>
 static void run_one(const kda::PackedParams &p, int warps) {
     using namespace kda;
     const int all = (p.Dv + kCW - 1) / kCW;
-    emu_poison((size_t)2 * kTPW * warps * token_floats(RPL * kRG, PER_HEAD) * sizeof(float));
+    emu_poison((size_t)(LOOP ? 2 : 1) * TPW * warps * token_floats(RPL * kRG, PER_HEAD) * sizeof(float));
     emu_launch(dim3(p.N * p.HV, (all + warps - 1) / warps), dim3(32 * warps),
-               [&] { packed_recurrent_kernel<Tin, RPL, PER_HEAD>(p); });
+               [&] { packed_recurrent_kernel<Tin, RPL, PER_HEAD, TPW, LOOP>(p); });
+}
+// warps = 0: every sequence fits one tile of a token per warp
+template <typename Tin, int RPL, bool PER_HEAD>
+static void run_len(const kda::PackedParams &p, int warps) {
+    if (warps == 0) run_one<Tin, RPL, PER_HEAD, 1, false>(p, (p.Dv + kda::kCW - 1) / kda::kCW);
+    else run_one<Tin, RPL, PER_HEAD, 2, true>(p, warps);
 }
 template <typename Tin>
 static void run_type(const kda::PackedParams &p, int warps) {
-    if (p.Dk <= 64) p.g_per_head ? run_one<Tin, 8, true>(p, warps) : run_one<Tin, 8, false>(p, warps);
-    else p.g_per_head ? run_one<Tin, 16, true>(p, warps) : run_one<Tin, 16, false>(p, warps);
+    if (p.Dk <= 64) p.g_per_head ? run_len<Tin, 8, true>(p, warps) : run_len<Tin, 8, false>(p, warps);
+    else p.g_per_head ? run_len<Tin, 16, true>(p, warps) : run_len<Tin, 16, false>(p, warps);
 }
 extern "C" int emu_packed_recurrent(kda::PackedParams *p, int bf16, int warps) {
     kda::g_packed_error = 0;

@@ -62,6 +62,7 @@ TOL = {"f32": 1e-5, "bf16": 2.0 ** -8 + 1e-5}
 PACK = dict(cu=[0, 3, 3, 20, 21, 40], slots=[2, 0, 5, -1, 1], fresh=[0, 1, 1, 0, 0], P=6)
 ODD = dict(cu=[2, 4, 9, 7, 30, 33], slots=[3, 3, 1, 9, 0], fresh=None, P=4)      # repeat, backwards, slot 9
 LONG = dict(cu=[0, 70, 199, 199, 226, 230], slots=[2, 0, 5, -1, 1], fresh=[0, 1, 1, 0, 0], P=6)
+FEW = dict(cu=[0, 8, 8, 9, 12], slots=[1, 0, -1, 2], fresh=[0, 0, 0, 1], P=3)
 STEP = dict(cu=None, slots=None, fresh=None, P=7)
 
 
@@ -167,6 +168,8 @@ CASES = [
     (run_delta, dict(pack=PACK, T=40, H=1, HV=1, Dk=65, Dv=36, dtype="bf16", gate="softplus", per_head=True, pad=3)),
     (run_delta, dict(pack=ODD, T=33, H=1, HV=2, Dk=16, Dv=4, dtype="f32", gate="softplus", per_head=False, warps=1)),
     (run_delta, dict(pack=STEP, T=5, H=2, HV=2, Dk=128, Dv=128, dtype="bf16", gate="bounded", per_head=False)),
+    (run_delta, dict(pack=STEP, T=5, H=1, HV=2, Dk=40, Dv=20, dtype="f32", gate="softplus", per_head=True, warps=0)),
+    (run_delta, dict(pack=FEW, T=12, H=1, HV=1, Dk=128, Dv=128, dtype="bf16", gate="bounded", per_head=False, warps=0)),
     (run_delta, dict(pack=PACK, T=43, H=1, HV=1, Dk=40, Dv=8, dtype="f32", gate="bounded", per_head=True,
                      flags=False, warps=1)),
     (run_delta, dict(pack=LONG, T=230, H=1, HV=2, Dk=128, Dv=128, dtype="bf16", gate="softplus", per_head=True,
@@ -192,7 +195,7 @@ CASES = [
     (run_norm, dict(N=1, L=300, C=48, G=1, dtype="bf16", act="none", gated=False, params=False)),
     (run_norm, dict(N=2, L=33, C=18, G=3, dtype="f32", act="sigmoid", gated=False)),
 ]
-RACES = (0, 1, 6, 10, 13, 15, 17, 20)
+RACES = (0, 1, 5, 8, 12, 15, 17, 19, 22)
 
 
 def load(path):

@@ -177,6 +177,12 @@ def test_known_longest_length_changes_nothing(cuda_device, name):
     assert torch.equal(a, b) and torch.equal(t["pool"], u["pool"])
 
 
+def test_wrong_longest_length(cuda_device):
+    """A longest length given too small costs time, not results."""
+    check(*batch(cuda_device, [30, 1, 17, 100], 1, 2, 128, 128, "bf16", "softplus", True), max_seqlen=1)
+    check(*batch(cuda_device, [30, 1, 17, 100], 1, 2, 40, 20, "f32", "bounded", False), max_seqlen=2)
+
+
 @pytest.mark.parametrize("switch", ["qk_l2norm_in_kernel", "beta_sigmoid_in_kernel"])
 def test_switches(cuda_device, switch):
     t, kw = batch(cuda_device, [6, 11], 1, 2, 32, 32, "f32", "bounded", False)
