@@ -168,13 +168,18 @@ def load():
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr()).value
+    return None if t is None else t.data_ptr() or None
 
 
 def _stream(stream, device):
     if stream is None:
         stream = torch.cuda.current_stream(device)
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _raw_stream(stream, index):
+    """_stream as a plain number, without making a stream object."""
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
 def _dtype_code(t):
@@ -187,6 +192,9 @@ def _dtype_code(t):
 
 def _check(t, name, shape, dtype, device):
     if t is None:
+        return
+    if (isinstance(t, torch.Tensor) and t.shape == shape and (dtype is None or t.dtype is dtype)
+            and t.device == device and t.is_contiguous()):
         return
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
@@ -222,6 +230,19 @@ def _call(name, dev, cfn, *args):
     on the wrong GPU.  Raises KdaError on a non-OK status."""
     with torch.cuda.device(dev):
         _raise(name, cfn(*args))
+
+
+def _launch(name, dev, cfn, args, stream):
+    """_call for the entry points whose host time shows: the current device is
+    changed only if it is another."""
+    index = dev.index
+    if torch._C._cuda_getDevice() == index:
+        status = cfn(args, _raw_stream(stream, index))
+    else:
+        with torch.cuda.device(index):
+            status = cfn(args, _raw_stream(stream, index))
+    if status != KDA_OK:
+        raise KdaError(name, status)
 
 
 def kda_chunk_fwd(q, k, v, g, beta, *, A_log=None, dt_bias=None, S0=None, chunk=64,
@@ -462,6 +483,10 @@ def kda_output_gate(o, gate, weight=None, *, eps=1e-6, y=None, stream=None):
 def _check_rows(t, name, shape, dtype, device):
     """As _check, for rows that may lie apart: every dimension but the first
     contiguous.  Returns the elements from one row to the next."""
+    row = shape[1] if len(shape) == 2 else shape[1] * shape[2]
+    if (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.device == device
+            and t.is_contiguous()):
+        return row
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if t.device != device:
@@ -470,9 +495,6 @@ def _check_rows(t, name, shape, dtype, device):
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
     if t.dtype != dtype:
         raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
-    row = 1
-    for d in shape[1:]:
-        row *= d
     if t.numel() and not t[0].is_contiguous():
         raise ValueError("the rows of %s must be contiguous" % name)
     if shape[0] <= 1 or t.numel() == 0:
@@ -524,33 +546,27 @@ def kda_packed_fwd(q, k, v, g, beta, pool, *, cu_seqlens=None, slots=None, fresh
     dev, dt = q.device, q.dtype
     T, H, Dk = q.shape
     P, HV, _, Dv = pool.shape
-    gk = () if g_per_head else (Dk,)
-    a = PackedArgs()
-    a.dtype = _dtype_code(q)
-    a.ld_q = _check_rows(q, "q", (T, H, Dk), dt, dev)
-    a.ld_k = _check_rows(k, "k", (T, H, Dk), dt, dev)
-    a.ld_v = _check_rows(v, "v", (T, HV, Dv), dt, dev)
-    a.ld_g = _check_rows(g, "g", (T, HV) + gk, dt, dev)
-    a.ld_beta = _check_rows(beta, "beta", (T, HV), dt, dev)
+    per_head = bool(g_per_head)
+    gshape, bshape = ((T, HV), (HV,)) if per_head else ((T, HV, Dk), (HV, Dk))
+    code = _dtype_code(q)
+    ld_q = _check_rows(q, "q", (T, H, Dk), dt, dev)
+    ld_k = _check_rows(k, "k", (T, H, Dk), dt, dev)
+    ld_v = _check_rows(v, "v", (T, HV, Dv), dt, dev)
+    ld_g = _check_rows(g, "g", gshape, dt, dev)
+    ld_b = _check_rows(beta, "beta", (T, HV), dt, dev)
     _check(pool, "pool", (P, HV, Dk, Dv), torch.float32, dev)
     _check(A_log, "A_log", (HV,), torch.float32, dev)
-    _check(dt_bias, "dt_bias", (HV,) + gk, torch.float32, dev)
+    _check(dt_bias, "dt_bias", bshape, torch.float32, dev)
     n, fresh = _check_packing(cu_seqlens, slots, fresh, T, dev)
     if o is None:
         o = torch.empty((T, HV, Dv), dtype=dt, device=dev)
-    a.ld_o = _check_rows(o, "o", (T, HV, Dv), dt, dev)
-    a.N, a.T, a.P, a.H, a.HV, a.Dk, a.Dv = n, T, P, H, HV, Dk, Dv
-    a.max_seqlen, a.algo = int(max_seqlen or 0), ALGOS[algo]
-    a.g_min, a.scale, a.l2_eps = float(g_min), float(scale), float(l2_eps)
-    a.qk_l2norm_in_kernel = int(bool(qk_l2norm_in_kernel))
-    a.beta_sigmoid_in_kernel = int(bool(beta_sigmoid_in_kernel))
-    a.gate_in_kernel = _gate_code(gate_in_kernel)
-    a.g_per_head = int(bool(g_per_head))
-    a.q, a.k, a.v, a.g, a.beta = map(_ptr, (q, k, v, g, beta))
-    a.A_log, a.dt_bias = _ptr(A_log), _ptr(dt_bias)
-    a.cu_seqlens, a.slots, a.fresh = _ptr(cu_seqlens), _ptr(slots), _ptr(fresh)
-    a.pool, a.o = _ptr(pool), _ptr(o)
-    _call("kda_packed_fwd", dev, lib.kda_packed_fwd, ctypes.byref(a), _stream(stream, dev))
+    ld_o = _check_rows(o, "o", (T, HV, Dv), dt, dev)
+    a = PackedArgs(n, T, P, H, HV, Dk, Dv, int(max_seqlen or 0), code, ALGOS[algo], g_min, scale, l2_eps,
+                   bool(qk_l2norm_in_kernel), bool(beta_sigmoid_in_kernel), _gate_code(gate_in_kernel), per_head,
+                   ld_q, ld_k, ld_v, ld_g, ld_b, ld_o, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+                   beta.data_ptr(), _ptr(A_log), _ptr(dt_bias), _ptr(cu_seqlens), _ptr(slots), _ptr(fresh),
+                   pool.data_ptr(), o.data_ptr())
+    _launch("kda_packed_fwd", dev, lib.kda_packed_fwd, a, stream)
     return o
 
 
@@ -566,22 +582,18 @@ def kda_packed_conv(x, w, pool, bias=None, *, cu_seqlens=None, slots=None, fresh
     dev, dt = x.device, x.dtype
     T, C = x.shape
     K, P = w.shape[1], pool.shape[0]
-    a = PackedConvArgs()
-    a.dtype = _dtype_code(x)
-    a.ld_x = _check_rows(x, "x", (T, C), dt, dev)
+    code = _dtype_code(x)
+    ld_x = _check_rows(x, "x", (T, C), dt, dev)
     _check(w, "w", (C, K), torch.float32, dev)
     _check(bias, "bias", (C,), torch.float32, dev)
     _check(pool, "pool", (P, K - 1, C), dt, dev)
     n, fresh = _check_packing(cu_seqlens, slots, fresh, T, dev)
     if y is None:
         y = torch.empty((T, C), dtype=dt, device=dev)
-    a.ld_y = _check_rows(y, "y", (T, C), dt, dev)
-    a.N, a.T, a.P, a.C, a.K = n, T, P, C, K
-    a.head_dim, a.silu, a.l2_eps = int(head_dim), int(bool(silu)), float(l2_eps)
-    a.x, a.w, a.bias = _ptr(x), _ptr(w), _ptr(bias)
-    a.cu_seqlens, a.slots, a.fresh = _ptr(cu_seqlens), _ptr(slots), _ptr(fresh)
-    a.pool, a.y = _ptr(pool), _ptr(y)
-    _call("kda_packed_conv", dev, lib.kda_packed_conv, ctypes.byref(a), _stream(stream, dev))
+    ld_y = _check_rows(y, "y", (T, C), dt, dev)
+    a = PackedConvArgs(n, T, P, C, K, int(head_dim), bool(silu), code, l2_eps, ld_x, ld_y, x.data_ptr(), w.data_ptr(),
+                       _ptr(bias), _ptr(cu_seqlens), _ptr(slots), _ptr(fresh), _ptr(pool), y.data_ptr())
+    _launch("kda_packed_conv", dev, lib.kda_packed_conv, a, stream)
     return y
 
 
@@ -601,14 +613,11 @@ def _group_norm_args(x, groups, weight, bias, gate, act):
     _check(gate, "gate", (N, L, C), dt, dev)
     _check(weight, "weight", (C,), torch.float32, dev)
     _check(bias, "bias", (C,), torch.float32, dev)
-    a = GroupNormArgs()
-    a.N, a.L, a.C, a.G, a.act, a.dtype = N, L, C, G, ACTS[act], _dtype_code(x)
-    a.x, a.gate, a.weight, a.bias = _ptr(x), _ptr(gate), _ptr(weight), _ptr(bias)
-    return a
+    return GroupNormArgs(N, L, C, G, ACTS[act], _dtype_code(x), 0.0, _ptr(x), _ptr(gate), _ptr(weight), _ptr(bias))
 
 
 def _group_norm_workspace(lib, a, backward, dev):
-    n = int(lib.kda_group_norm_workspace(a.N, a.L, a.C, a.G, a.dtype, int(backward)))
+    n = lib.kda_group_norm_workspace(a.N, a.L, a.C, a.G, a.dtype, backward)
     return torch.empty(n, dtype=torch.uint8, device=dev) if n else None
 
 
@@ -626,12 +635,11 @@ def kda_group_norm_fwd(x, groups, weight=None, bias=None, gate=None, *, act="non
     if y is None:
         y = torch.empty_like(x)
     _check(y, "y", tuple(x.shape), x.dtype, dev)
-    mean = torch.empty((a.N, a.G), dtype=torch.float32, device=dev)
-    rstd = torch.empty((a.N, a.G), dtype=torch.float32, device=dev)
+    mean, rstd = torch.empty((2, a.N, a.G), dtype=torch.float32, device=dev).unbind()
     ws = _group_norm_workspace(lib, a, False, dev)
     a.eps = float(eps)
     a.y, a.mean, a.rstd, a.workspace = _ptr(y), _ptr(mean), _ptr(rstd), _ptr(ws)
-    _call("kda_group_norm_fwd", dev, lib.kda_group_norm_fwd, ctypes.byref(a), _stream(stream, dev))
+    _launch("kda_group_norm_fwd", dev, lib.kda_group_norm_fwd, a, stream)
     return y, mean, rstd
 
 
@@ -655,7 +663,7 @@ def kda_group_norm_bwd(dy, x, groups, mean, rstd, weight=None, bias=None, gate=N
     a.dy, a.mean, a.rstd, a.workspace = _ptr(dy), _ptr(mean), _ptr(rstd), _ptr(ws)
     for name, t in out.items():
         setattr(a, name, _ptr(t))
-    _call("kda_group_norm_bwd", dev, lib.kda_group_norm_bwd, ctypes.byref(a), _stream(stream, dev))
+    _launch("kda_group_norm_bwd", dev, lib.kda_group_norm_bwd, a, stream)
     return out
 
 
