@@ -3,12 +3,13 @@
 //
 //     u[t] = bias + sum_j w[j] x[t - (K-1) + j],  y = u * sigmoid(u),  y / |y|_head
 //
-// A lane owns 8 channels and walks a run of rows with the window in registers,
-// so every row of x is read once (and K - 1 rows again where a run begins); a
-// warp covers 256 channels, 16 lanes a head of 128.  Rows before a sequence's
-// first come from its slot.  The run that holds a sequence's first row also
-// does the K - 2 rows behind it and writes the slot's new window, after its
-// own read of the old one: nobody else reads the slot.
+// A lane owns 8 channels and walks a run of rows with the last four in a ring of
+// registers (four rows unrolled, so that no row is ever moved), so every row of x
+// is read once (and K - 1 rows again where a run begins); a warp covers 256
+// channels, 16 lanes a head of 128.  Rows before a sequence's first come from its
+// slot.  The run that holds a sequence's first row also does the K - 2 rows behind
+// it and writes the slot's new window, after its own read of the old one: nobody
+// else reads the slot.
 #include "kda_packed.cuh"
 
 namespace kda {
@@ -65,10 +66,24 @@ template <> struct Raw8<float> {
     }
 };
 
-// exp for SiLU: the library function in fp32; for bf16 rows the hardware
-// approximation, whose error (below 2^-20 here) vanishes in the rounding.
-__device__ __forceinline__ float exp_for(const float *, float x) { return expf(x); }
-__device__ __forceinline__ float exp_for(const __nv_bfloat16 *, float x) { return __expf(x); }
+// u * sigmoid(u): library exp and division in fp32; for bf16 rows the hardware
+// approximations, whose error (below 2^-20 here) vanishes in the rounding.
+__device__ __forceinline__ float silu_for(const float *, float u) { return u / (1.f + expf(-u)); }
+__device__ __forceinline__ float silu_for(const __nv_bfloat16 *, float u) { return __fdividef(u, 1.f + __expf(-u)); }
+
+// The last sequence that begins at or before `row` (0 if none does): 32 bounds at a time.
+__device__ __forceinline__ int find_sequence(const int *cu, int n, int row, int lane) {
+    int lo = 0, len = n;                   // the answer is in [lo, lo + len)
+    while (len > 1) {
+        const int step = (len + 31) / 32, at = lo + lane * step;
+        const bool le = lane * step < len && cu[at] <= row;
+        const int k = __popc(__ballot_sync(0xffffffffu, le)) - 1;     // bounds do not decrease
+        if (k < 0) return 0;
+        lo += k * step;
+        len = min(step, len - k * step);
+    }
+    return lo;
+}
 
 template <typename Tin, int K>
 __global__ void __launch_bounds__(kThreads)
@@ -92,22 +107,29 @@ packed_conv_kernel(const PackedConvParams p, int run) {
 
     const Tin *x = static_cast<const Tin *>(p.x) + c;
     Tin *y = static_cast<Tin *>(p.y) + c;
-    float w[K][8], bias[8];
+    float2 w[K][4], bias[4];               // channel pairs
+    {
+        const float *wc = p.w + (size_t)c * K;
+        float wf[8 * K];
+        if (reinterpret_cast<uintptr_t>(p.w) % 16 == 0) {        // 8 K floats from a multiple of 8 K
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < 2 * K; ++i) {
+                const float4 f = c_ok ? *reinterpret_cast<const float4 *>(wc + 4 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
+                wf[4 * i] = f.x; wf[4 * i + 1] = f.y; wf[4 * i + 2] = f.z; wf[4 * i + 3] = f.w;
+            }
+        } else {
 #pragma unroll
-        for (int j = 0; j < K; ++j) w[j][i] = c_ok ? p.w[(size_t)(c + i) * K + j] : 0.f;
-        bias[i] = c_ok && p.bias ? p.bias[c + i] : 0.f;
+            for (int i = 0; i < 8 * K; ++i) wf[i] = c_ok ? wc[i] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int j = 0; j < K; ++j) w[j][i] = make_float2(wf[2 * i * K + j], wf[(2 * i + 1) * K + j]);
+            bias[i] = c_ok && p.bias ? make_float2(p.bias[c + 2 * i], p.bias[c + 2 * i + 1]) : make_float2(0.f, 0.f);
+        }
     }
 
-    // the last sequence that begins at or before r0
-    int lo = 0, hi = p.N - 1;
-    while (p.cu && lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (p.cu[mid] <= r0) lo = mid; else hi = mid - 1;
-    }
-    if (!p.cu) lo = r0;
-    for (int s = lo; s < p.N; ++s) {
+    for (int s = p.cu ? find_sequence(p.cu, p.N, r0, lane) : r0; s < p.N; ++s) {
         const PackedSeq sq = packed_seq(p.cu, p.slots, p.T, p.P, s);
         if (sq.bad || sq.len == 0) continue;
         const int b = sq.begin, e = b + sq.len;
@@ -117,6 +139,13 @@ packed_conv_kernel(const PackedConvParams p, int run) {
         const int own = b >= r0 && b + W > r1 ? b + W : r1;
         const int end = e < own ? e : own;
         if (row >= end) continue;
+        Raw8<Tin> ahead[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            ahead[u].zero();
+            if (c_ok && row + u < end) ahead[u].load(x + (long long)(row + u) * p.ldx);
+        }
+        const bool zero = p.fresh && p.fresh[s];
         const bool repeat = __any_sync(0xffffffffu, packed_repeat(p.slots, s, sq.slot, lane, 32));
         if (repeat) {
             if (row == b && lane == 0) atomicOr(&g_packed_conv_error, kPackedRange);
@@ -124,10 +153,9 @@ packed_conv_kernel(const PackedConvParams p, int run) {
         }
         if (sq.slot < 0) continue;
 
-        // window before `row`
+        // ring[(u - i) & 3]: the row i before row u of a block of four; the window before `row`
         Tin *slot = static_cast<Tin *>(p.pool) + (size_t)sq.slot * W * p.C + c;
-        const bool zero = p.fresh && p.fresh[s];
-        float win[W > 0 ? W : 1][8];
+        float2 ring[4][4];
         Raw8<Tin> raw[W > 0 ? W : 1];
 #pragma unroll
         for (int j = 0; j < W; ++j) {
@@ -137,7 +165,10 @@ packed_conv_kernel(const PackedConvParams p, int run) {
                 if (t >= b) raw[j].load(x + (long long)t * p.ldx);
                 else if (!zero) raw[j].load(slot + (size_t)(t - b + W) * p.C);
             }
-            raw[j].get(win[j]);
+            float f[8];
+            raw[j].get(f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ring[(4 - W + j) & 3][i] = make_float2(f[2 * i], f[2 * i + 1]);
         }
         if (row == b) {                    // raw holds the whole old window
 #pragma unroll
@@ -156,48 +187,42 @@ packed_conv_kernel(const PackedConvParams p, int run) {
             }
         }
 
-        Raw8<Tin> ahead[kAhead];
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            ahead[u].zero();
-            if (c_ok && row + u < end) ahead[u].load(x + (long long)(row + u) * p.ldx);
-        }
         for (; row < end; row += kAhead) {
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
-                float cur[8], f[8];
-                ahead[u].get(cur);
+                {
+                    float cur[8];
+                    ahead[u].get(cur);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) ring[u][i] = make_float2(cur[2 * i], cur[2 * i + 1]);
+                }
                 if (c_ok && row + u + kAhead < end) ahead[u].load(x + (long long)(row + u + kAhead) * p.ldx);
+                float2 f[4];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float a = fmaf(w[K - 1][i], cur[i], bias[i]);
+                for (int i = 0; i < 4; ++i) {
+                    f[i] = bias[i];
 #pragma unroll
-                    for (int j = 0; j < W; ++j) a = fmaf(w[j][i], win[j][i], a);
-                    f[i] = a;
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-#pragma unroll
-                    for (int j = 0; j + 1 < W; ++j) win[j][i] = win[j + 1][i];
-                    if (W > 0) win[W > 0 ? W - 1 : 0][i] = cur[i];
-                }
-                if (p.silu) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) f[i] = f[i] / (1.f + exp_for(static_cast<Tin *>(nullptr), -f[i]));
+                    for (int j = 0; j < K; ++j) f[i] = __ffma2_rn(w[j][i], ring[(u + 4 - W + j) & 3][i], f[i]);
+                    if (p.silu) {
+                        f[i].x = silu_for(static_cast<Tin *>(nullptr), f[i].x);
+                        f[i].y = silu_for(static_cast<Tin *>(nullptr), f[i].y);
+                    }
                 }
                 if (p.head_dim) {
-                    float q = 0.f;
+                    float2 q = __fmul2_rn(f[0], f[0]);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) q = fmaf(f[i], f[i], q);
+                    for (int i = 1; i < 4; ++i) q = __ffma2_rn(f[i], f[i], q);
+                    float ss = q.x + q.y;
 #pragma unroll
-                    for (int off = 8; off > 0; off >>= 1) q += __shfl_xor_sync(0xffffffffu, q, off);
-                    const float r = 1.f / sqrtf(q + p.l2_eps);
+                    for (int off = 8; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+                    const float r = rsqrtf(ss + p.l2_eps);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) f[i] *= r;
+                    for (int i = 0; i < 4; ++i) f[i] = __fmul2_rn(f[i], make_float2(r, r));
                 }
                 if (c_ok && row + u < end) {
+                    const float out[8] = {f[0].x, f[0].y, f[1].x, f[1].y, f[2].x, f[2].y, f[3].x, f[3].y};
                     Raw8<Tin> o;
-                    o.set(f);
+                    o.set(out);
                     o.store(y + (long long)(row + u) * p.ldy);
                 }
             }

@@ -20,6 +20,14 @@ inline int __any_sync(unsigned m, int pred) {
     for (int off = 16; off > 0; off >>= 1) r += __shfl_xor_sync(m, r, off);
     return r != 0.f;
 }
+inline unsigned __ballot_sync(unsigned m, int pred) {
+    unsigned r = 0;
+    const int lane = threadIdx.x & 31;
+    for (int x = 0; x < 32; ++x)
+        if (__shfl_xor_sync(m, pred ? 1.f : 0.f, x) != 0.f) r |= 1u << (lane ^ x);
+    return r;
+}
+inline int __popc(unsigned v) { return __builtin_popcount(v); }
 // Any other lane's value, in xor steps: the lanes meet five times.
 inline float emu_lane_value(unsigned m, float v, int src) {
     const int lane = threadIdx.x & 31;
