@@ -70,7 +70,7 @@ template <typename Tin> struct Vec<Tin, 1> {
 // approximations, whose error (below 2^-20) vanishes in the rounding to 8 bits.
 template <typename Tin> __device__ __forceinline__ float sig(float u) { return 1.f / (1.f + expf(-u)); }
 template <> __device__ __forceinline__ float sig<__nv_bfloat16>(float u) {
-    return __fdividef(1.f, 1.f + __expf(-u));
+    return rcpf_(1.f + ex2f_(-kLog2E * u));
 }
 template <typename Tin> __device__ __forceinline__ float act_f(int act, float u) {
     if (act == 0) return u;

@@ -35,6 +35,18 @@ __device__ __forceinline__ float ex2f_(float x) {
 #endif
 }
 
+// 1 / x on the special-function unit (PTX rcp.approx, one ulp; results below the
+// normal range flush to 0).
+__device__ __forceinline__ float rcpf_(float x) {
+#ifdef __CUDA_ARCH__
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+#else
+    return 1.0f / x;
+#endif
+}
+
 // Bounded log-decay g = g_min * sigmoid(exp(A_log) * (z + dt_bias)); `ea` is exp(A_log).
 __device__ __forceinline__ float bounded_gate(float z, float bias, float ea, float g_min) {
     return g_min * sigmoidf_(ea * (z + bias));

@@ -58,7 +58,13 @@ __device__ __forceinline__ PackedSeq packed_seq(const int *cu, const int *slots,
 __device__ __forceinline__ bool packed_repeat(const int *slots, int s, int slot, int tid, int step) {
     bool hit = false;
     if (slots && slot >= 0)
-        for (int i = tid; i < s; i += step) hit |= slots[i] == slot;
+        for (int i = tid; i < s; i += 8 * step) {
+            int v[8];                      // loads in flight together
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = i + k * step < s ? slots[i + k * step] : -1;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) hit |= v[k] == slot;
+        }
     return hit;
 }
 

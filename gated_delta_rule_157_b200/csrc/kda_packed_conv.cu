@@ -4,7 +4,7 @@
 //     u[t] = bias + sum_j w[j] x[t - (K-1) + j],  y = u * sigmoid(u),  y / |y|_head
 //
 // A lane owns 8 channels and walks a run of rows with the last four in a ring of
-// registers (four rows unrolled, so that no row is ever moved), so every row of x
+// registers (four rows unrolled, so that no row is moved), so every row of x
 // is read once (and K - 1 rows again where a run begins); a warp covers 256
 // channels, 16 lanes a head of 128.  Rows before a sequence's first come from its
 // slot.  The run that holds a sequence's first row also does the K - 2 rows behind
@@ -18,7 +18,6 @@ namespace {
 __device__ unsigned int g_packed_conv_error = 0;
 
 constexpr int kThreads = 128;
-constexpr int kAhead = 4;                  // rows requested ahead of the one computed
 
 // Eight channels as they lie in memory, and in fp32.
 template <typename Tin> struct Raw8;
@@ -69,7 +68,7 @@ template <> struct Raw8<float> {
 // u * sigmoid(u): library exp and division in fp32; for bf16 rows the hardware
 // approximations, whose error (below 2^-20 here) vanishes in the rounding.
 __device__ __forceinline__ float silu_for(const float *, float u) { return u / (1.f + expf(-u)); }
-__device__ __forceinline__ float silu_for(const __nv_bfloat16 *, float u) { return __fdividef(u, 1.f + __expf(-u)); }
+__device__ __forceinline__ float silu_for(const __nv_bfloat16 *, float u) { return u * rcpf_(1.f + ex2f_(-kLog2E * u)); }
 
 // The last sequence that begins at or before `row` (0 if none does): 32 bounds at a time.
 __device__ __forceinline__ int find_sequence(const int *cu, int n, int row, int lane) {
@@ -85,8 +84,9 @@ __device__ __forceinline__ int find_sequence(const int *cu, int n, int row, int 
     return lo;
 }
 
-template <typename Tin, int K>
-__global__ void __launch_bounds__(kThreads)
+// kAhead: rows done together, and requested ahead: 4, or 1 where runs are single rows.
+template <typename Tin, int K, int kAhead>
+__global__ void __launch_bounds__(kThreads, sizeof(Tin) == 2 ? 4 : 1)
 packed_conv_kernel(const PackedConvParams p, int run) {
     constexpr int W = K - 1;
     const int lane = threadIdx.x & 31;
@@ -125,7 +125,18 @@ packed_conv_kernel(const PackedConvParams p, int run) {
         for (int i = 0; i < 4; ++i) {
 #pragma unroll
             for (int j = 0; j < K; ++j) w[j][i] = make_float2(wf[2 * i * K + j], wf[(2 * i + 1) * K + j]);
-            bias[i] = c_ok && p.bias ? make_float2(p.bias[c + 2 * i], p.bias[c + 2 * i + 1]) : make_float2(0.f, 0.f);
+            bias[i] = make_float2(0.f, 0.f);
+        }
+        if (c_ok && p.bias) {
+            if (reinterpret_cast<uintptr_t>(p.bias) % 16 == 0) {
+                const float4 b0 = *reinterpret_cast<const float4 *>(p.bias + c);
+                const float4 b1 = *reinterpret_cast<const float4 *>(p.bias + c + 4);
+                bias[0] = make_float2(b0.x, b0.y); bias[1] = make_float2(b0.z, b0.w);
+                bias[2] = make_float2(b1.x, b1.y); bias[3] = make_float2(b1.z, b1.w);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) bias[i] = make_float2(p.bias[c + 2 * i], p.bias[c + 2 * i + 1]);
+            }
         }
     }
 
@@ -187,60 +198,90 @@ packed_conv_kernel(const PackedConvParams p, int run) {
             }
         }
 
+        // Four rows at a time, step by step for all four: their chains of special
+        // functions and shuffles overlap.
         for (; row < end; row += kAhead) {
+            float2 f[kAhead][4];
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
-                {
-                    float cur[8];
-                    ahead[u].get(cur);
+                float cur[8];
+                ahead[u].get(cur);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) ring[u][i] = make_float2(cur[2 * i], cur[2 * i + 1]);
-                }
+                for (int i = 0; i < 4; ++i) ring[u][i] = make_float2(cur[2 * i], cur[2 * i + 1]);
                 if (c_ok && row + u + kAhead < end) ahead[u].load(x + (long long)(row + u + kAhead) * p.ldx);
-                float2 f[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    f[i] = bias[i];
+                    f[u][i] = bias[i];
 #pragma unroll
-                    for (int j = 0; j < K; ++j) f[i] = __ffma2_rn(w[j][i], ring[(u + 4 - W + j) & 3][i], f[i]);
-                    if (p.silu) {
-                        f[i].x = silu_for(static_cast<Tin *>(nullptr), f[i].x);
-                        f[i].y = silu_for(static_cast<Tin *>(nullptr), f[i].y);
+                    for (int j = 0; j < K; ++j) f[u][i] = __ffma2_rn(w[j][i], ring[(u + 4 - W + j) & 3][i], f[u][i]);
+                }
+            }
+            if (p.silu) {
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        f[u][i].x = silu_for(static_cast<Tin *>(nullptr), f[u][i].x);
+                        f[u][i].y = silu_for(static_cast<Tin *>(nullptr), f[u][i].y);
                     }
+            }
+            if (p.head_dim) {
+                float ss[kAhead];
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    float2 q = __fmul2_rn(f[u][0], f[u][0]);
+#pragma unroll
+                    for (int i = 1; i < 4; ++i) q = __ffma2_rn(f[u][i], f[u][i], q);
+                    ss[u] = q.x + q.y;
                 }
-                if (p.head_dim) {
-                    float2 q = __fmul2_rn(f[0], f[0]);
 #pragma unroll
-                    for (int i = 1; i < 4; ++i) q = __ffma2_rn(f[i], f[i], q);
-                    float ss = q.x + q.y;
+                for (int off = 8; off > 0; off >>= 1)
 #pragma unroll
-                    for (int off = 8; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-                    const float r = rsqrtf(ss + p.l2_eps);
+                    for (int u = 0; u < kAhead; ++u) ss[u] += __shfl_xor_sync(0xffffffffu, ss[u], off);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) f[i] = __fmul2_rn(f[i], make_float2(r, r));
+                for (int u = 0; u < kAhead; ++u) {
+                    const float r = rsqrtf(ss[u] + p.l2_eps);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) f[u][i] = __fmul2_rn(f[u][i], make_float2(r, r));
                 }
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
                 if (c_ok && row + u < end) {
-                    const float out[8] = {f[0].x, f[0].y, f[1].x, f[1].y, f[2].x, f[2].y, f[3].x, f[3].y};
+                    const float out[8] = {f[u][0].x, f[u][0].y, f[u][1].x, f[u][1].y,
+                                          f[u][2].x, f[u][2].y, f[u][3].x, f[u][3].y};
                     Raw8<Tin> o;
                     o.set(out);
                     o.store(y + (long long)(row + u) * p.ldy);
+                }
+            if (kAhead == 1) {             // no ring to come round: the rows move
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    ring[1][i] = ring[2][i];
+                    ring[2][i] = ring[3][i];
+                    ring[3][i] = ring[0][i];
                 }
             }
         }
     }
 }
 
-template <typename Tin>
-cudaError_t launch_type(const PackedConvParams &p, int run, cudaStream_t s) {
+template <typename Tin, int K>
+cudaError_t launch_taps(const PackedConvParams &p, int run, cudaStream_t s) {
     const long long warps = ((long long)p.T + run - 1) / run * ((p.C + 255) / 256);
     const unsigned grid = (unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32));
-    switch (p.K) {
-        case 1: packed_conv_kernel<Tin, 1><<<grid, kThreads, 0, s>>>(p, run); break;
-        case 2: packed_conv_kernel<Tin, 2><<<grid, kThreads, 0, s>>>(p, run); break;
-        case 3: packed_conv_kernel<Tin, 3><<<grid, kThreads, 0, s>>>(p, run); break;
-        default: packed_conv_kernel<Tin, 4><<<grid, kThreads, 0, s>>>(p, run); break;
-    }
+    if (run == 1) packed_conv_kernel<Tin, K, 1><<<grid, kThreads, 0, s>>>(p, run);
+    else packed_conv_kernel<Tin, K, 4><<<grid, kThreads, 0, s>>>(p, run);
     return cudaGetLastError();
+}
+template <typename Tin>
+cudaError_t launch_type(const PackedConvParams &p, int run, cudaStream_t s) {
+    switch (p.K) {
+        case 1: return launch_taps<Tin, 1>(p, run, s);
+        case 2: return launch_taps<Tin, 2>(p, run, s);
+        case 3: return launch_taps<Tin, 3>(p, run, s);
+    }
+    return launch_taps<Tin, 4>(p, run, s);
 }
 
 }  // namespace

@@ -88,12 +88,16 @@ static void run_conv(const kda::PackedConvParams &p, int run) {
     emu_poison(0);
     const long long warps = ((long long)p.T + run - 1) / run * ((p.C + 255) / 256);
     const dim3 grid((unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32)));
+#define KDA_RUN(K) \
+    if (run == 1) emu_launch(grid, dim3(kThreads), [&] { packed_conv_kernel<Tin, K, 1>(p, run); }); \
+    else emu_launch(grid, dim3(kThreads), [&] { packed_conv_kernel<Tin, K, 4>(p, run); })
     switch (p.K) {
-        case 1: emu_launch(grid, dim3(kThreads), [&] { packed_conv_kernel<Tin, 1>(p, run); }); break;
-        case 2: emu_launch(grid, dim3(kThreads), [&] { packed_conv_kernel<Tin, 2>(p, run); }); break;
-        case 3: emu_launch(grid, dim3(kThreads), [&] { packed_conv_kernel<Tin, 3>(p, run); }); break;
-        default: emu_launch(grid, dim3(kThreads), [&] { packed_conv_kernel<Tin, 4>(p, run); }); break;
+        case 1: KDA_RUN(1); break;
+        case 2: KDA_RUN(2); break;
+        case 3: KDA_RUN(3); break;
+        default: KDA_RUN(4); break;
     }
+#undef KDA_RUN
 }
 extern "C" int emu_packed_conv(kda::PackedConvParams *p, int bf16, int run) {
     kda::g_packed_conv_error = 0;
