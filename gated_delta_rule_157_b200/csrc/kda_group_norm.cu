@@ -112,6 +112,19 @@ __device__ __forceinline__ void slab_sum2(float &a, float &b, int tps) {
     }
 }
 
+__device__ __forceinline__ float slab_sum(float a, int tps) {
+    for (int off = (tps < 32 ? tps : 32) >> 1; off > 0; off >>= 1) a += __shfl_xor_sync(0xffffffffu, a, off);
+    if (tps > 32) {
+        const int warp = threadIdx.x >> 5, per = tps >> 5, first = warp / per * per;
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) smem[warp] = a;
+        __syncthreads();
+        a = 0.f;
+        for (int i = 0; i < per; ++i) a += smem[first + i];
+    }
+    return a;
+}
+
 // ------------------------------------------------------------- held form
 template <typename Tin, int VEC, int VPT>
 struct HeldPlace {
@@ -164,7 +177,7 @@ gn_held_fwd_kernel(const GroupNormParams p, const GroupNormPlan pl) {
         const int n = n0 + at.sub;
         const bool on = at.on && n < p.N;
         float v[VPT][VEC], z[VPT][VEC];
-        float sum = 0.f, none = 0.f;
+        float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             if (at.off[i] >= 0 && on) {
@@ -178,8 +191,7 @@ gn_held_fwd_kernel(const GroupNormParams p, const GroupNormPlan pl) {
             for (int j = 0; j < VEC; ++j) sum += v[i][j];
         }
         request(n + step);
-        slab_sum2(sum, none, pl.tps);
-        const float mean = sum * inv;
+        const float mean = slab_sum(sum, pl.tps) * inv;
         float m2 = 0.f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
@@ -190,8 +202,7 @@ gn_held_fwd_kernel(const GroupNormParams p, const GroupNormPlan pl) {
                     m2 = fmaf(v[i][j], v[i][j], m2);
                 }
             }
-        slab_sum2(m2, none, pl.tps);
-        const float rstd = 1.f / sqrtf(fmaf(m2, inv, p.eps));
+        const float rstd = 1.f / sqrtf(fmaf(slab_sum(m2, pl.tps), inv, p.eps));
         if (!on) continue;
         Tin *y = static_cast<Tin *>(p.y) + n * row;
 #pragma unroll
@@ -321,26 +332,27 @@ gn_held_bwd_kernel(const GroupNormParams p, const GroupNormPlan pl) {
 }
 
 // out[k][c] = sum over the `rows` partial rows ws[row][k][c], in a fixed order:
-// 8 threads per channel, each every eighth row.
-__global__ void __launch_bounds__(kThreads)
+// 32 threads per channel, each every 32nd row.
+constexpr int kSumThreads = 1024;
+__global__ void __launch_bounds__(kSumThreads)
 gn_sum_kernel(const float *ws, int rows, int C, float *dw, float *db) {
     const int c = blockIdx.x * 32 + (threadIdx.x & 31), part = threadIdx.x >> 5;
     float a = 0.f, b = 0.f;
     if (c < C) {
 #pragma unroll 4
-        for (int r = part; r < rows; r += 8) {
+        for (int r = part; r < rows; r += 32) {
             a += ws[((size_t)r * 2 + 0) * C + c];
             b += ws[((size_t)r * 2 + 1) * C + c];
         }
     }
     smem[threadIdx.x] = a;
-    smem[kThreads + threadIdx.x] = b;
+    smem[kSumThreads + threadIdx.x] = b;
     __syncthreads();
     if (part == 0 && c < C) {
         a = b = 0.f;
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < 32; ++k) {
             a += smem[32 * k + threadIdx.x];
-            b += smem[kThreads + 32 * k + threadIdx.x];
+            b += smem[kSumThreads + 32 * k + threadIdx.x];
         }
         if (dw) dw[c] = a;
         if (db) db[c] = b;
@@ -352,9 +364,11 @@ gn_sum_kernel(const float *ws, int rows, int C, float *dw, float *db) {
 // slab row n = x / tiles.  Thread = (vector, row lane).
 struct TilePlace {
     int n, l0, l1, cv, rl, lanes;
-    __device__ __forceinline__ TilePlace(const GroupNormParams &p, const GroupNormPlan &pl) {
-        n = blockIdx.x / pl.tiles;
-        const int tile = blockIdx.x % pl.tiles;
+    // The last pass goes backwards: what the first read last is still in L2.
+    __device__ __forceinline__ TilePlace(const GroupNormParams &p, const GroupNormPlan &pl, bool backwards = false) {
+        const int x = backwards ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+        n = x / pl.tiles;
+        const int tile = x % pl.tiles;
         l0 = tile * pl.rt;
         l1 = min(l0 + pl.rt, p.L);
         cv = blockIdx.y * pl.cvb + threadIdx.x % pl.cvb;
@@ -417,14 +431,13 @@ gn_tile_mean_kernel(const GroupNormParams p, const GroupNormPlan pl) {
     const float *ws = p.ws + (size_t)n * pl.tiles * 2 * p.C + (size_t)g * p.D;
     const int items = pl.tiles * p.D;
     const float inv = 1.f / ((float)p.L * (float)p.D);
-    float sum = 0.f, none = 0.f;
+    float sum = 0.f;
     for (int i = threadIdx.x; i < items; i += kThreads) {
         const int t = i / p.D, d = i - t * p.D;
         const float cnt = (float)(min((t + 1) * pl.rt, p.L) - t * pl.rt);
         sum = fmaf(cnt, ws[(size_t)t * 2 * p.C + d], sum);
     }
-    slab_sum2(sum, none, kThreads);
-    const float mean = sum * inv;
+    const float mean = slab_sum(sum, kThreads) * inv;
     float m2 = 0.f;
     for (int i = threadIdx.x; i < items; i += kThreads) {
         const int t = i / p.D, d = i - t * p.D;
@@ -432,7 +445,7 @@ gn_tile_mean_kernel(const GroupNormParams p, const GroupNormPlan pl) {
         const float e = ws[(size_t)t * 2 * p.C + d] - mean;
         m2 += fmaf(cnt * e, e, ws[((size_t)t * 2 + 1) * p.C + d]);
     }
-    slab_sum2(m2, none, kThreads);
+    m2 = slab_sum(m2, kThreads);
     if (threadIdx.x == 0) {
         p.mean[(size_t)n * p.G + g] = mean;
         p.rstd[(size_t)n * p.G + g] = 1.f / sqrtf(fmaf(m2, inv, p.eps));
@@ -442,7 +455,7 @@ gn_tile_mean_kernel(const GroupNormParams p, const GroupNormPlan pl) {
 template <typename Tin, int VEC, bool GATED>
 __global__ void __launch_bounds__(kThreads)
 gn_tile_fwd_kernel(const GroupNormParams p, const GroupNormPlan pl) {
-    const TilePlace at(p, pl);
+    const TilePlace at(p, pl, true);
     if (at.cv * VEC >= p.C) return;
     const long long base = (long long)at.n * p.L * p.C + (long long)at.cv * VEC;
     float w[VEC], b[VEC], m[VEC];
@@ -556,7 +569,7 @@ gn_tile_gsum_kernel(const GroupNormParams p, const GroupNormPlan pl, float *out)
 template <typename Tin, int VEC, bool GATED>
 __global__ void __launch_bounds__(kThreads)
 gn_tile_bwd_kernel(const GroupNormParams p, const GroupNormPlan pl, const float *gsum) {
-    const TilePlace at(p, pl);
+    const TilePlace at(p, pl, true);
     if (at.cv * VEC >= p.C) return;
     const long long base = (long long)at.n * p.L * p.C + (long long)at.cv * VEC;
     float w[VEC], b[VEC], m[VEC], r[VEC], s1[VEC], s2[VEC];
@@ -598,6 +611,7 @@ gn_tile_bwd_kernel(const GroupNormParams p, const GroupNormPlan pl, const float 
 
 constexpr size_t kHeldSmem = (64 + 2 * kThreads) * sizeof(float);
 constexpr size_t kTileSmem = 2 * kThreads * sizeof(float);
+constexpr size_t kSumSmem = 2 * kSumThreads * sizeof(float);
 
 template <typename Tin, int VEC, int VPT>
 cudaError_t launch_held_fwd(const GroupNormParams &p, const GroupNormPlan &pl, cudaStream_t s) {
@@ -616,7 +630,7 @@ cudaError_t launch_held(const GroupNormParams &p, const GroupNormPlan &pl, bool 
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     if (p.dweight || p.dbias) {
-        gn_sum_kernel<<<(p.C + 31) / 32, kThreads, kTileSmem, s>>>(p.ws, pl.gy, p.C, p.dweight, p.dbias);
+        gn_sum_kernel<<<(p.C + 31) / 32, kSumThreads, kSumSmem, s>>>(p.ws, pl.gy, p.C, p.dweight, p.dbias);
         e = cudaGetLastError();
     }
     return e;
@@ -637,7 +651,7 @@ cudaError_t launch_tiled(const GroupNormParams &p, const GroupNormPlan &pl, bool
     else gn_tile_dsum_kernel<Tin, VEC, false><<<grid, kThreads, kTileSmem, s>>>(p, pl);
     gn_tile_gsum_kernel<<<p.N * p.G, kThreads, kTileSmem, s>>>(p, pl, gsum);
     if (p.dweight || p.dbias)
-        gn_sum_kernel<<<(p.C + 31) / 32, kThreads, kTileSmem, s>>>(p.ws, p.N * pl.tiles, p.C, p.dweight, p.dbias);
+        gn_sum_kernel<<<(p.C + 31) / 32, kSumThreads, kSumSmem, s>>>(p.ws, p.N * pl.tiles, p.C, p.dweight, p.dbias);
     if (p.dx || p.dgate) {
         if (p.gate) gn_tile_bwd_kernel<Tin, VEC, true><<<grid, kThreads, 0, s>>>(p, pl, gsum);
         else gn_tile_bwd_kernel<Tin, VEC, false><<<grid, kThreads, 0, s>>>(p, pl, gsum);
@@ -674,7 +688,9 @@ int pow2_at_least(int x) {
 GroupNormPlan group_norm_plan(int N, int L, int C, int G, bool bf16, bool backward, bool aligned) {
     GroupNormPlan pl = {};
     const int D = C / G, full = bf16 ? 8 : 4;
-    const long long slots = 148ll * 8;     // blocks of 256 threads that the device holds at once
+    // blocks of 256 threads that are resident at once (registers allow four of the
+    // forward, two of the backward): more would only be more partial rows
+    const long long slots = 148ll * (backward ? 2 : 4);
     // held: vectors lie inside a group
     const int hv = aligned && D % full == 0 ? full : 1;
     const long long nvec = (long long)L * D / hv;
@@ -703,7 +719,7 @@ GroupNormPlan group_norm_plan(int N, int L, int C, int G, bool bf16, bool backwa
     pl.gy = (cv + pl.cvb - 1) / pl.cvb;
     const int lanes = kThreads / pl.cvb;
     pl.rt = 256;
-    while (pl.rt > 4 * lanes && pl.rt > 16 && (long long)N * ((L + pl.rt - 1) / pl.rt) * pl.gy < slots) pl.rt /= 2;
+    while (pl.rt > 4 * lanes && pl.rt > 16 && (long long)N * ((L + pl.rt - 1) / pl.rt) * pl.gy < 148 * 4) pl.rt /= 2;
     if (pl.rt > L) pl.rt = L;
     pl.tiles = (L + pl.rt - 1) / pl.rt;
     pl.gx = N * pl.tiles;
