@@ -27,6 +27,7 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kRows = 4;                   // rows a thread requests together
 extern __shared__ float smem[];
 
 template <typename Tin, int VEC> struct Vec;
@@ -504,25 +505,33 @@ gn_tile_dsum_kernel(const GroupNormParams p, const GroupNormPlan pl) {
         sh[j] = su[j] = 0.f;
     }
     if (in) {
-#pragma unroll 2
-        for (int l = at.l0 + at.rl; l < at.l1; l += at.lanes) {
-            Vec<Tin, VEC> v, dv, zv;
-            float f[VEC], g[VEC], z[VEC];
-            const long long o = base + (long long)l * p.C;
-            v.load(static_cast<const Tin *>(p.x) + o);
-            dv.load(static_cast<const Tin *>(p.dy) + o);
-            if (GATED) zv.load(static_cast<const Tin *>(p.gate) + o);
-            v.get(f);
-            dv.get(g);
-            if (GATED) zv.get(z);
+        Vec<Tin, VEC> v[kRows], dv[kRows], zv[kRows];
+        for (int l = at.l0 + at.rl; l < at.l1; l += kRows * at.lanes) {
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                const float h = (f[j] - m[j]) * r[j];
-                float a, d;
-                act_fd<Tin>(p.act, GATED ? z[j] : fmaf(h, w[j], b[j]), a, d);
-                const float du = g[j] * (GATED ? a : d);
-                su[j] += du;
-                sh[j] = fmaf(du, h, sh[j]);
+            for (int q = 0; q < kRows; ++q) {
+                const int r = l + q * at.lanes;
+                if (r >= at.l1) break;
+                const long long o = base + (long long)r * p.C;
+                v[q].load(static_cast<const Tin *>(p.x) + o);
+                dv[q].load(static_cast<const Tin *>(p.dy) + o);
+                if (GATED) zv[q].load(static_cast<const Tin *>(p.gate) + o);
+            }
+#pragma unroll
+            for (int q = 0; q < kRows; ++q) {
+                if (l + q * at.lanes >= at.l1) break;
+                float f[VEC], g[VEC], z[VEC];
+                v[q].get(f);
+                dv[q].get(g);
+                if (GATED) zv[q].get(z);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    const float h = (f[j] - m[j]) * r[j];
+                    float a, d;
+                    act_fd<Tin>(p.act, GATED ? z[j] : fmaf(h, w[j], b[j]), a, d);
+                    const float du = g[j] * (GATED ? a : d);
+                    su[j] += du;
+                    sh[j] = fmaf(du, h, sh[j]);
+                }
             }
         }
     }
@@ -584,28 +593,38 @@ gn_tile_bwd_kernel(const GroupNormParams p, const GroupNormPlan pl, const float 
         s1[j] = gsum[2 * ng];
         s2[j] = gsum[2 * ng + 1];
     }
-#pragma unroll 2
-    for (int l = at.l0 + at.rl; l < at.l1; l += at.lanes) {
-        Vec<Tin, VEC> v, dv, zv;
-        float f[VEC], g[VEC], z[VEC];
-        const long long o = base + (long long)l * p.C;
-        v.load(static_cast<const Tin *>(p.x) + o);
-        dv.load(static_cast<const Tin *>(p.dy) + o);
-        if (GATED) zv.load(static_cast<const Tin *>(p.gate) + o);
-        v.get(f);
-        dv.get(g);
-        if (GATED) zv.get(z);
+    Vec<Tin, VEC> v[kRows], dv[kRows], zv[kRows];
+    for (int l = at.l0 + at.rl; l < at.l1; l += kRows * at.lanes) {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            const float h = (f[j] - m[j]) * r[j], u = fmaf(h, w[j], b[j]);
-            float a, d;
-            act_fd<Tin>(p.act, GATED ? z[j] : u, a, d);
-            const float du = g[j] * (GATED ? a : d);
-            if (GATED) z[j] = g[j] * u * d;
-            f[j] = r[j] * (fmaf(du, w[j], -s1[j]) - h * s2[j]);
+        for (int q = 0; q < kRows; ++q) {
+            const int row = l + q * at.lanes;
+            if (row >= at.l1) break;
+            const long long o = base + (long long)row * p.C;
+            v[q].load(static_cast<const Tin *>(p.x) + o);
+            dv[q].load(static_cast<const Tin *>(p.dy) + o);
+            if (GATED) zv[q].load(static_cast<const Tin *>(p.gate) + o);
         }
-        if (p.dx) Vec<Tin, VEC>::put(static_cast<Tin *>(p.dx) + o, f);
-        if (GATED && p.dgate) Vec<Tin, VEC>::put(static_cast<Tin *>(p.dgate) + o, z);
+#pragma unroll
+        for (int q = 0; q < kRows; ++q) {
+            const int row = l + q * at.lanes;
+            if (row >= at.l1) break;
+            const long long o = base + (long long)row * p.C;
+            float f[VEC], g[VEC], z[VEC];
+            v[q].get(f);
+            dv[q].get(g);
+            if (GATED) zv[q].get(z);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                const float h = (f[j] - m[j]) * r[j], u = fmaf(h, w[j], b[j]);
+                float a, d;
+                act_fd<Tin>(p.act, GATED ? z[j] : u, a, d);
+                const float du = g[j] * (GATED ? a : d);
+                if (GATED) z[j] = g[j] * u * d;
+                f[j] = r[j] * (fmaf(du, w[j], -s1[j]) - h * s2[j]);
+            }
+            if (p.dx) Vec<Tin, VEC>::put(static_cast<Tin *>(p.dx) + o, f);
+            if (GATED && p.dgate) Vec<Tin, VEC>::put(static_cast<Tin *>(p.dgate) + o, z);
+        }
     }
 }
 
