@@ -480,7 +480,7 @@ static kda_status group_norm(const kda_group_norm_args *a, void *stream, bool ba
     const size_t es = bf16 ? 2 : 4;
     const size_t nx = (size_t)a->N * a->L * a->C * es, nc = (size_t)a->C * 4, ns = (size_t)a->N * a->G * 4;
     // the grid's limit, and the element counts of a slab that the kernels keep in an int
-    if ((long long)a->N * a->L > 0x7FFFFFFFll || (long long)a->N * a->G > 0x7FFFFFFFll ||
+    if ((long long)a->N * a->L > 0x7FFFFFFFll || (long long)a->N * a->G + a->C > 0x7FFFFFFFll ||
         (long long)a->L * (a->C / a->G) > 0x7FFFFFFFll)
         return KDA_ERR_UNSUPPORTED;
     if (backward && a->dgate && !a->gate) return KDA_ERR_INVALID_ARG;

@@ -333,11 +333,10 @@ gn_held_bwd_kernel(const GroupNormParams p, const GroupNormPlan pl) {
 }
 
 // out[k][c] = sum over the `rows` partial rows ws[row][k][c], in a fixed order:
-// 32 threads per channel, each every 32nd row.
+// 32 threads per channel, each every 32nd row; block = 32 channels.
 constexpr int kSumThreads = 1024;
-__global__ void __launch_bounds__(kSumThreads)
-gn_sum_kernel(const float *ws, int rows, int C, float *dw, float *db) {
-    const int c = blockIdx.x * 32 + (threadIdx.x & 31), part = threadIdx.x >> 5;
+__device__ __forceinline__ void sum_rows(const float *ws, int rows, int C, float *dw, float *db, int block) {
+    const int c = block * 32 + (threadIdx.x & 31), part = threadIdx.x >> 5;
     float a = 0.f, b = 0.f;
     if (c < C) {
 #pragma unroll 4
@@ -358,6 +357,10 @@ gn_sum_kernel(const float *ws, int rows, int C, float *dw, float *db) {
         if (dw) dw[c] = a;
         if (db) db[c] = b;
     }
+}
+__global__ void __launch_bounds__(kSumThreads)
+gn_sum_kernel(const float *ws, int rows, int C, float *dw, float *db) {
+    sum_rows(ws, rows, C, dw, db, blockIdx.x);
 }
 
 // ------------------------------------------------------------- tiled form
@@ -554,20 +557,26 @@ gn_tile_dsum_kernel(const GroupNormParams p, const GroupNormPlan pl) {
     }
 }
 
-// mean(dh), mean(dh h) of (n, g), behind the partial sums in ws.
-__global__ void __launch_bounds__(kThreads)
+// Blocks up to N * G: mean(dh), mean(dh h) of one (n, g), behind the partial sums
+// in ws; the blocks behind them: dweight and dbias of 32 channels each.
+__global__ void __launch_bounds__(kSumThreads)
 gn_tile_gsum_kernel(const GroupNormParams p, const GroupNormPlan pl, float *out) {
+    if ((long long)blockIdx.x >= (long long)p.N * p.G) {
+        sum_rows(p.ws, p.N * pl.tiles, p.C, p.dweight, p.dbias, (int)(blockIdx.x - (unsigned)(p.N * p.G)));
+        return;
+    }
     const int n = blockIdx.x / p.G, g = blockIdx.x % p.G;
     const float *ws = p.ws + (size_t)n * pl.tiles * 2 * p.C + (size_t)g * p.D;
     const int items = pl.tiles * p.D;
     float s1 = 0.f, s2 = 0.f;
-    for (int i = threadIdx.x; i < items; i += kThreads) {
+#pragma unroll 4
+    for (int i = threadIdx.x; i < items; i += kSumThreads) {
         const int t = i / p.D, d = i - t * p.D;
         const float w = p.weight ? p.weight[g * p.D + d] : 1.f;
         s2 = fmaf(w, ws[(size_t)t * 2 * p.C + d], s2);
         s1 = fmaf(w, ws[((size_t)t * 2 + 1) * p.C + d], s1);
     }
-    slab_sum2(s1, s2, kThreads);
+    slab_sum2(s1, s2, kSumThreads);
     if (threadIdx.x == 0) {
         const float inv = 1.f / ((float)p.L * (float)p.D);
         out[2 * ((size_t)n * p.G + g)] = s1 * inv;
@@ -668,9 +677,8 @@ cudaError_t launch_tiled(const GroupNormParams &p, const GroupNormPlan &pl, bool
     float *gsum = p.ws + (size_t)p.N * pl.tiles * 2 * p.C;
     if (p.gate) gn_tile_dsum_kernel<Tin, VEC, true><<<grid, kThreads, kTileSmem, s>>>(p, pl);
     else gn_tile_dsum_kernel<Tin, VEC, false><<<grid, kThreads, kTileSmem, s>>>(p, pl);
-    gn_tile_gsum_kernel<<<p.N * p.G, kThreads, kTileSmem, s>>>(p, pl, gsum);
-    if (p.dweight || p.dbias)
-        gn_sum_kernel<<<(p.C + 31) / 32, kSumThreads, kSumSmem, s>>>(p.ws, p.N * pl.tiles, p.C, p.dweight, p.dbias);
+    const unsigned sums = p.dweight || p.dbias ? (unsigned)((p.C + 31) / 32) : 0u;
+    gn_tile_gsum_kernel<<<(unsigned)(p.N * p.G) + sums, kSumThreads, kSumSmem, s>>>(p, pl, gsum);
     if (p.dx || p.dgate) {
         if (p.gate) gn_tile_bwd_kernel<Tin, VEC, true><<<grid, kThreads, 0, s>>>(p, pl, gsum);
         else gn_tile_bwd_kernel<Tin, VEC, false><<<grid, kThreads, 0, s>>>(p, pl, gsum);
@@ -737,9 +745,11 @@ GroupNormPlan group_norm_plan(int N, int L, int C, int G, bool bf16, bool backwa
     if (pl.cvb > kThreads) pl.cvb = kThreads;
     pl.gy = (cv + pl.cvb - 1) / pl.cvb;
     const int lanes = kThreads / pl.cvb;
-    pl.rt = 256;
-    while (pl.rt > 4 * lanes && pl.rt > 16 && (long long)N * ((L + pl.rt - 1) / pl.rt) * pl.gy < 148 * 4) pl.rt /= 2;
-    if (pl.rt > L) pl.rt = L;
+    // as many tiles as make one round of resident blocks, of 4 rows a thread or more
+    long long tiles = slots / ((long long)N * pl.gy);
+    if (tiles > (L + 4 * lanes - 1) / (4 * lanes)) tiles = (L + 4 * lanes - 1) / (4 * lanes);
+    if (tiles < 1) tiles = 1;
+    pl.rt = (int)((L + tiles - 1) / tiles);
     pl.tiles = (L + pl.rt - 1) / pl.rt;
     pl.gx = N * pl.tiles;
     pl.ws_floats = (size_t)N * pl.tiles * 2 * C + (size_t)N * G * 2;

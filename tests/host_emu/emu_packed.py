@@ -140,10 +140,8 @@ static void run_tiled(const kda::GroupNormParams &p, const kda::GroupNormPlan &p
     }
     float *gsum = p.ws + (size_t)p.N * pl.tiles * 2 * p.C;
     emu_launch(grid, dim3(kThreads), [&] { gn_tile_dsum_kernel<Tin, VEC, GATED>(p, pl); });
-    emu_launch(dim3(p.N * p.G), dim3(kThreads), [&] { gn_tile_gsum_kernel(p, pl, gsum); });
     emu_poison(kSumSmem);
-    emu_launch(dim3((p.C + 31) / 32), dim3(kSumThreads),
-               [&] { gn_sum_kernel(p.ws, p.N * pl.tiles, p.C, p.dweight, p.dbias); });
+    emu_launch(dim3(p.N * p.G + (p.C + 31) / 32), dim3(kSumThreads), [&] { gn_tile_gsum_kernel(p, pl, gsum); });
     emu_poison(kTileSmem);
     emu_launch(grid, dim3(kThreads), [&] { gn_tile_bwd_kernel<Tin, VEC, GATED>(p, pl, gsum); });
 }
