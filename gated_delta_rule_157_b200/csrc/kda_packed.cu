@@ -8,8 +8,8 @@
 //
 // so one pass over the registers and one reduction serve both.  State columns
 // are independent: a warp owns CW = 4 * 32 / RG columns of all Dk rows, lane =
-// (row group, quad of columns); only the RG row groups meet, in log2(RG)
-// shuffle steps, and no warp waits for another inside a tile of tokens.  What
+// (row group, quad of columns); only the RG row groups meet, in seven
+// exchanges and four broadcasts a token, and no warp waits for another inside a tile of tokens.  What
 // depends on the token alone (norms, gates, ka, qa) is prepared by the block
 // for a tile of TPW tokens per warp.  Long sequences (LOOP) prepare two tokens
 // a warp into a double shared buffer, the next tile's rows requested while one is
@@ -195,34 +195,38 @@ packed_recurrent_kernel(const PackedParams p) {
                     aq[c] = __ffma2_rn(make_float2(q4.z, q4.w), st[2 * i + 1][c], aq[c]);
                 }
             }
-            float ks[4], qs[4];
+            // Sums over the row groups, scattered: of the eight (S^T ka, S^T qa per
+            // column) each group ends with one -- group c with S^T ka of column c,
+            // group 4 + c with S^T qa of it -- in 4 + 2 + 1 exchanges.
+            float r[8];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                ks[c] = ak[c].x + ak[c].y;
-                qs[c] = aq[c].x + aq[c].y;
+                r[c] = ak[c].x + ak[c].y;
+                r[4 + c] = aq[c].x + aq[c].y;
             }
 #pragma unroll
-            for (int off = 32 / kRG; off < 32; off <<= 1) {
+            for (int half = 4; half > 0; half >>= 1) {
+                const bool up = rg & half;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    ks[c] += __shfl_xor_sync(0xffffffffu, ks[c], off);
-                    qs[c] += __shfl_xor_sync(0xffffffffu, qs[c], off);
+                for (int c = 0; c < half; ++c) {
+                    const float send = up ? r[c] : r[half + c], keep = up ? r[half + c] : r[c];
+                    r[c] = keep + __shfl_xor_sync(0xffffffffu, send, half * (32 / kRG));
                 }
             }
             const float *xv = x + (PER_HEAD ? 2 : 4) * DKP;
             const float beta = xv[128], qk = xv[129], ah = xv[130];
-            float u[4], ov = 0.f;
+            const int c = rg & 3;
+            const float dot = PER_HEAD ? ah * r[0] : r[0];
+            const float mine_u = beta * (xv[(col & 127) + c] - dot);       // of use in the groups below 4
+            float u[4], uc = 0.f;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const float e = xv[(col & 127) + c] - (PER_HEAD ? ah * ks[c] : ks[c]);
-                u[c] = beta * e;
-                const float oc = fmaf(qk, u[c], PER_HEAD ? ah * qs[c] : qs[c]);
-                ov = rg == c ? oc : ov;
+            for (int k = 0; k < 4; ++k) {
+                u[k] = __shfl_sync(0xffffffffu, mine_u, k * (32 / kRG) + quad);
+                uc = c == k ? u[k] : uc;
             }
-            // row group c writes column c of the quad
-            if (rg < 4 && col_ok)
+            if (rg >= 4 && col_ok)
                 st_act(static_cast<Tin *>(p.o) + ((long long)sq.begin + t0 + t) * p.ldo + (long long)hv * p.Dv,
-                       (size_t)(col + rg), ov);
+                       (size_t)(col + c), fmaf(qk, uc, dot));
 #pragma unroll
             for (int i = 0; i < RPL / 4; ++i) {
                 const float4 k4 = *reinterpret_cast<const float4 *>((PER_HEAD ? xk : xk + 2 * DKP) + i * 4 * kRG);
@@ -230,10 +234,10 @@ packed_recurrent_kernel(const PackedParams p) {
                 if (!PER_HEAD) a4 = *reinterpret_cast<const float4 *>(xk + 3 * DKP + i * 4 * kRG);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    const float2 uc = make_float2(u[c], u[c]);
-                    st[2 * i][c] = __ffma2_rn(make_float2(k4.x, k4.y), uc,
+                    const float2 u2 = make_float2(u[c], u[c]);
+                    st[2 * i][c] = __ffma2_rn(make_float2(k4.x, k4.y), u2,
                                               __fmul2_rn(make_float2(a4.x, a4.y), st[2 * i][c]));
-                    st[2 * i + 1][c] = __ffma2_rn(make_float2(k4.z, k4.w), uc,
+                    st[2 * i + 1][c] = __ffma2_rn(make_float2(k4.z, k4.w), u2,
                                                   __fmul2_rn(make_float2(a4.z, a4.w), st[2 * i + 1][c]));
                 }
             }
