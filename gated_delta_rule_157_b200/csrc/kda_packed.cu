@@ -36,7 +36,7 @@ template <typename Tin, int RPL, bool PER_HEAD>
 struct TokenPrep {
     static constexpr int DKP = RPL * kRG;
     static constexpr int NC = (DKP + 31) / 32;
-    float q[NC], k[NC], g[NC], v[4], beta;
+    Tin q0[NC], k0[NC], g0[NC], v0[4], beta0;      // as loaded: a conversion would wait for the load
 
     __device__ __forceinline__ void load(const PackedParams &p, long long row, int h, int hv, int lane) {
         const Tin *qr = static_cast<const Tin *>(p.q) + row * p.ldq + (long long)h * p.Dk;
@@ -46,19 +46,33 @@ struct TokenPrep {
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = lane + 32 * i;
-            const bool in = c < p.Dk;
-            q[i] = in ? ld_act(qr, c) : 0.f;
-            k[i] = in ? ld_act(kr, c) : 0.f;
-            if (!PER_HEAD) g[i] = in ? ld_act(gr, c) : 0.f;
+            if (c < p.Dk) {
+                q0[i] = qr[c];
+                k0[i] = kr[c];
+                if (!PER_HEAD) g0[i] = gr[c];
+            }
         }
-        if (PER_HEAD) g[0] = ld_act(gr, 0);
+        if (PER_HEAD) g0[0] = gr[0];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = lane + 32 * i < p.Dv ? ld_act(vr, lane + 32 * i) : 0.f;
-        beta = ld_act(static_cast<const Tin *>(p.beta) + row * p.ldb, hv);
+        for (int i = 0; i < 4; ++i)
+            if (lane + 32 * i < p.Dv) v0[i] = vr[lane + 32 * i];
+        beta0 = static_cast<const Tin *>(p.beta)[row * p.ldb + hv];
     }
 
     // `bias`: dt_bias of this lane's channels, 0 beyond them.
     __device__ __forceinline__ void store(const PackedParams &p, const float (&bias)[NC], float ea, int lane, float *out) {
+        float q[NC], k[NC], g[NC], v[4];
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const bool in = lane + 32 * i < p.Dk;
+            q[i] = in ? ld_act(&q0[i], 0) : 0.f;
+            k[i] = in ? ld_act(&k0[i], 0) : 0.f;
+            g[i] = in && !PER_HEAD ? ld_act(&g0[i], 0) : 0.f;
+        }
+        if (PER_HEAD) g[0] = ld_act(&g0[0], 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = lane + 32 * i < p.Dv ? ld_act(&v0[i], 0) : 0.f;
+        const float beta = ld_act(&beta0, 0);
         float sq = 0.f, sk = 0.f, qk = 0.f;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
