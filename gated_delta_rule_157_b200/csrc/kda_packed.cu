@@ -294,7 +294,7 @@ cudaError_t launch_len(const PackedParams &p, int max_len, cudaStream_t s) {
     const int all = (p.Dv + kCW - 1) / kCW;
     if (max_len <= 4 && all > 4) return launch_one<Tin, RPL, PER_HEAD, 1, false>(p, 4, s);
     if (max_len <= all) return launch_one<Tin, RPL, PER_HEAD, 1, false>(p, all, s);
-    return launch_one<Tin, RPL, PER_HEAD, 2, true>(p, all < 4 ? all : 4, s);
+    return launch_one<Tin, RPL, PER_HEAD, 2, true>(p, all, s);
 }
 
 template <typename Tin>
