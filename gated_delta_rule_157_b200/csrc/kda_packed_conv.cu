@@ -10,6 +10,11 @@
 // slot.  The run that holds a sequence's first row also does the K - 2 rows behind
 // it and writes the slot's new window, after its own read of the old one: nobody
 // else reads the slot.
+//
+// 16391 rows of 4096 channels take 75 us, 3.6 TB/s of 6.55: two special functions
+// a value (30 us of that unit alone) and 16 warps an SM, which 128 registers
+// allow.  A run is as long as leaves 16 warps an SM, 32 rows at most: a short run
+// reads K - 1 rows again.
 #include "kda_packed.cuh"
 
 namespace kda {

@@ -27,17 +27,30 @@
 // its norm at decays around e^-1 a token, by 1e-6 with hardly any decay; two
 // terms throughout would leave 3e-6 to 6e-6.
 //
-// One CTA per SM walks (sequence, head) chains.  8 state warps (thread = value
-// channel and half of the key channels; TMEM lane = value channel) run the
+// One CTA per SM walks (sequence, head) chains, longest first.  8 state warps
+// (thread = value channel = TMEM lane, and half of the key channels) run the
 // serial part; two groups of 4 prep warps build T Diag(beta), B and the row
 // factors of the chunks ahead, one the even, the other the odd chunks, so that
-// each has two chunks' time for its chain of small dependent steps.  All MMAs
-// are transposed (D = value channels x tokens or key channels), so S^T, R^T,
-// U^T are A operands in TMEM and K, Q, T, B are B operands in shared memory;
-// the K tile, loaded once by TMA with the 128-byte swizzle, serves K-major
-// (P, K K^T) and MN-major (dS).  Operand terms replace the accumulator columns
-// that the same thread has just read, so the state warps need three barriers a
-// chunk on the serial path.
+// each has two chunks' time for its chain of small dependent steps; a warp each
+// evaluates their gates; one warp, the oldest, issues every load and MMA.  All
+// MMAs are transposed (D = value channels x tokens or key channels), so S^T,
+// R^T, U^T are A operands in TMEM and K, Q, T, B are B operands in shared memory;
+// the K tile, loaded once by TMA with the 128-byte swizzle, serves K-major (P,
+// K K^T) and MN-major (dS).  Operand terms replace the accumulator columns that
+// the same thread has just read, so the state warps meet only at the mbarriers
+// of the issuing warp.
+//
+// What bounds it: the chain of one chunk, about 11,000 cycles: P 800, O of the
+// chunk before 1,000 and its stores 800, R 2,000, U 1,500, its terms 1,200, dS
+// 1,400, S and its terms 1,300, hand-overs the rest.  The tensor pipe is 33 %
+// busy (3,300 cycles of MMAs a chunk), issue slots 45 %, DRAM 12 %.  32768 rows x
+// 32 heads in 4 sequences: 0.745 ms, 1.10 TB/s.  What brought it there from 1.69
+// ms: shared-memory addresses formed without a trip through an integer (accesses
+// had become generic ones, and registers spilled), a warp that only issues, gates
+// off the prep groups' path, no barrier among the state warps.  Measured and not
+// kept: 4 state warps of whole rows (0.80 ms), 32-column TMEM accesses with 8
+// (0.79, registers spill), P for Q beside the split of U (the MMAs and the
+// warps' TMEM accesses slow each other).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
