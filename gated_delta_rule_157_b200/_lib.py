@@ -8,6 +8,7 @@ CPU path.  If the shared object is missing it is built with nvcc; if that
 fails, the import fails.
 """
 import ctypes
+import functools
 import os
 
 import torch
@@ -230,6 +231,18 @@ def _call(name, dev, cfn, *args):
     on the wrong GPU.  Raises KdaError on a non-OK status."""
     with torch.cuda.device(dev):
         _raise(name, cfn(*args))
+
+
+def _on_stream(fn):
+    """Runs a binding whose outputs and workspace it allocates itself on the
+    stream it was given, so that they belong to that stream."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        with torch.cuda.stream(stream):
+            return fn(*args, stream=stream, **kw)
+    return call
 
 
 def _launch(name, dev, cfn, args, stream):
@@ -519,6 +532,7 @@ def _check_packing(cu_seqlens, slots, fresh, rows, dev):
     return n, fresh
 
 
+@_on_stream
 def kda_packed_fwd(q, k, v, g, beta, pool, *, cu_seqlens=None, slots=None, fresh=None, max_seqlen=None,
                    A_log=None, dt_bias=None, g_min=-5.0, scale=1.0, l2_eps=1e-6, qk_l2norm_in_kernel=True,
                    beta_sigmoid_in_kernel=True, gate_in_kernel=True, g_per_head=False, algo="auto", o=None,
@@ -570,6 +584,7 @@ def kda_packed_fwd(q, k, v, g, beta, pool, *, cu_seqlens=None, slots=None, fresh
     return o
 
 
+@_on_stream
 def kda_packed_conv(x, w, pool, bias=None, *, cu_seqlens=None, slots=None, fresh=None, head_dim=0, silu=True,
                     l2_eps=1e-6, y=None, stream=None):
     """kda_short_conv over a packed batch: x [T,C] float32 or bfloat16 (C % 128
@@ -621,6 +636,7 @@ def _group_norm_workspace(lib, a, backward, dev):
     return torch.empty(n, dtype=torch.uint8, device=dev) if n else None
 
 
+@_on_stream
 def kda_group_norm_fwd(x, groups, weight=None, bias=None, gate=None, *, act="none", eps=1e-5, y=None, stream=None):
     """Group norm with an activation over channels-last rows: statistics over
     the L rows and C / groups channels of each (n, group), then
@@ -643,6 +659,7 @@ def kda_group_norm_fwd(x, groups, weight=None, bias=None, gate=None, *, act="non
     return y, mean, rstd
 
 
+@_on_stream
 def kda_group_norm_bwd(dy, x, groups, mean, rstd, weight=None, bias=None, gate=None, *, act="none", want_dx=True,
                        want_dgate=True, want_params=True, stream=None):
     """Gradient of kda_group_norm_fwd with the same arguments, from the mean and

@@ -219,3 +219,23 @@ def test_empty_batch(cuda_device):
     d = kda.kda_group_norm_bwd(x, x, 4, m, r, w, w)
     torch.cuda.synchronize()
     assert (d["dweight"] == 0).all() and (d["dbias"] == 0).all()
+
+
+def test_given_stream_owns_what_is_allocated(cuda_device):
+    """stream= runs the call, its outputs and its workspace on that stream, with
+    the current stream busy over memory that it has just freed."""
+    x, dy, z, w, b = inputs(cuda_device, 3, 900, 128, "bf16", True)
+    want = packed.group_norm(to_np(x), 4, to_np(w), to_np(b), to_np(z), "silu")[0]
+    g = packed.group_norm_backward(to_np(dy), to_np(x), 4, to_np(w), to_np(b), to_np(z), "silu")
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        junk = [torch.full((3, 900, 128), float(i), device=cuda_device) for i in range(8)]
+        del junk
+        y, m, r = kda.kda_group_norm_fwd(x, 4, w, b, z, act="silu", stream=s)
+        d = kda.kda_group_norm_bwd(dy, x, 4, m, r, w, b, z, act="silu", stream=s)
+        junk = [torch.full((3, 900, 128), float(i), device=cuda_device) for i in range(8)]
+        s.synchronize()
+        close(y, want)
+        close(d["dx"], g["dx"])
+        close(d["dweight"], g["dweight"], g["l1"].max())

@@ -351,6 +351,12 @@ def test_long_pool_offsets(cuda_device):
     close(t["pool"][P - 2:], pool)
 
 
+def test_more_sequences_than_pages_in_one_decode_batch(cuda_device):
+    """Hundreds of single rows beside a few long ones, lengths unknown to the host."""
+    lens = [1] * 300 + [70, 40] + [2] * 100 + [90]
+    check(*batch(cuda_device, lens, 1, 1, 128, 128, "bf16", "softplus", True))
+
+
 # ------------------------------------------------------------- convolution
 def conv_batch(dev, lens, C, K, dtype, seed=0, pad=0, slots=None, fresh=None, P=None, behind=0):
     gen = torch.Generator().manual_seed(seed)
