@@ -1211,6 +1211,13 @@ cudaError_t launch_packed_chunk(const PackedParams &p, cudaStream_t s) {
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(packed_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
     if (e != cudaSuccess) return e;
+    // The roles' registers add up to kLaunchRegs a thread: a build that launches with
+    // fewer would wait for ever for the increase.
+    static const int regs = []() {
+        cudaFuncAttributes at;
+        return cudaFuncGetAttributes(&at, packed_chunk_kernel) == cudaSuccess ? at.numRegs : 0;
+    }();
+    if (regs < kLaunchRegs) return cudaErrorInvalidConfiguration;
     PackedTcParams tp;
     tp.p = p;
     if ((e = make_map(&tp.tm[0], p.k, p.H, p.T, p.ldk, true)) != cudaSuccess) return e;
