@@ -18,14 +18,17 @@
 //
 // Precision.  K and Q enter the products as they are given (bf16, unscaled:
 // norms and decays are applied to rows of the fp32 results), so K K^T, Q K^T
-// are exact products.  What is fp32 enters as a sum of bf16 terms (head, tail,
-// ...: 8 bits each).  R, U' = Diag(c) U and T Diag(beta) take three terms (24
-// bits), S two where it is multiplied by K or Q (its 2^-18 reaches the state
-// only through U, weighed by the decay; the state itself lives in fp32
-// registers, S = gamma S + dS with dS from the MMA), B and the U of O two (O
-// is rounded to bf16).  Simulated over 16 chunks the state is off by 5e-8 of
-// its norm at decays around e^-1 a token, by 1e-6 with hardly any decay; two
-// terms throughout would leave 3e-6 to 6e-6.
+// are exact products.  What is fp32 -- S, R, U, U' = Diag(c) U, T Diag(beta), B --
+// enters as the sum of three bf16 terms (head, middle, tail: 24 bits).  S and U' meet
+// K or Q, which have one term: theirs are cut off one after another, and nothing is
+// left over.  Where both sides are split the terms are rounded, which leaves the
+// smallest middle and tail, and the six products of the larger orders are taken; what
+// is left out is 2^-26 of a product.  The state itself lives in fp32 registers, S =
+// gamma S + dS with dS from the MMA.  Simulated over 16 chunks the splits leave the
+// state off by 5e-8 to 7e-8 of its norm (an fp32 recurrence on the same inputs by
+// 5e-7), and 1 in 10^4 of the bf16 outputs differs from the rounded exact one.  Two
+// terms of S would leave 1.3e-6 with hardly any decay, two of S, B and the U of O 3
+// outputs in 10^3, for 0.75 ms instead of 0.81 on 32768 rows x 32 heads.
 //
 // One CTA per SM walks (sequence, head) chains, longest first.  8 state warps
 // (thread = value channel = TMEM lane, and half of the key channels) run the
@@ -40,17 +43,16 @@
 // the same thread has just read, so the state warps meet only at the mbarriers
 // of the issuing warp.
 //
-// What bounds it: the chain of one chunk, about 11,000 cycles: P 800, O of the
-// chunk before 1,000 and its stores 800, R 2,000, U 1,500, its terms 1,200, dS
-// 1,400, S and its terms 1,300, hand-overs the rest.  The tensor pipe is 33 %
-// busy (3,300 cycles of MMAs a chunk), issue slots 45 %, DRAM 12 %.  32768 rows x
-// 32 heads in 4 sequences: 0.745 ms, 1.10 TB/s.  What brought it there from 1.69
-// ms: shared-memory addresses formed without a trip through an integer (accesses
-// had become generic ones, and registers spilled), a warp that only issues, gates
-// off the prep groups' path, no barrier among the state warps.  Measured and not
-// kept: 4 state warps of whole rows (0.80 ms), 32-column TMEM accesses with 8
-// (0.79, registers spill), P for Q beside the split of U (the MMAs and the
-// warps' TMEM accesses slow each other).
+// What bounds it: the chain of one chunk, about 11,500 cycles: what is left of P 700,
+// O of the chunk before 800 and its stores 1,000, R 1,900, U 1,700, its terms for dS
+// 1,100, dS 1,500, S and its terms 1,300, their stores 1,300 (the MMAs and the warps'
+// TMEM accesses slow each other).  DRAM 12 %.  32768 rows x 32 heads in 4 sequences:
+// 0.81 ms, 1.0 TB/s.  What shortened it: shared-memory addresses formed without a
+// trip through an integer (accesses had become generic ones, and registers
+// spilled), a warp that only issues, gates off the prep groups' path, no barrier
+// among the state warps, U' before U.  Measured and not kept: 4 state warps of whole
+// rows, 32-column TMEM accesses (registers spill), P for Q beside the split of U,
+// the next K and Q requested behind P instead of ahead of it.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -76,8 +78,9 @@ constexpr int kStages = 3;                 // of K, Q; of B and the row factors
 constexpr uint32_t OFF_KQ = 0;
 constexpr uint32_t OFF_V = OFF_KQ + kStages * KQ_BYTES;        // [64][128] bf16
 constexpr uint32_t OFF_TB = OFF_V + 16384;                       // 3 terms of T Diag(beta), 64 x 64
-constexpr uint32_t OFF_AQK = OFF_TB + 3 * 8192;                  // stages x 2 terms of B
-constexpr uint32_t OFF_A = OFF_AQK + kStages * 2 * 8192;         // per group: A, then T, fp32
+constexpr uint32_t OFF_AQK = OFF_TB + 3 * 8192;                  // stages x 3 terms of B, lower blocks only
+constexpr uint32_t B_BYTES = 16384;
+constexpr uint32_t OFF_A = OFF_AQK + kStages * B_BYTES;          // per group: A, then T, fp32
 constexpr uint32_t A_BYTES = C * LDA * 4;
 constexpr uint32_t OFF_VEC = OFF_A + 2 * A_BYTES;                // stages x {-fk[64], fq[64], c[64], gamma}
 constexpr uint32_t VEC_BYTES = 1024;
@@ -93,24 +96,32 @@ static_assert(SMEM_BYTES <= 232448, "shared memory of one CTA");
 // prep group done with them; READY: prep of a chunk done;
 // FREE: its B and row factors used; TBFREE: its T used.  KK: [K ; Q] K^T done;
 // KKFREE: read.  S: P, U, dS done, in turn; Q: Pq done; O: O done.  From the state
-// warps, one arrival each: ST terms of S written, RT of R, UT of U and U'; OT the
+// warps, one arrival each: ST terms of S written, RT of R, UD of U', UT of U; OT the
 // O before taken.
 enum {
     MB_KQ = 0, MB_V = 3, MB_READY = 4, MB_FREE = 6, MB_KK = 9, MB_KKFREE = 11, MB_S = 13, MB_O = 14,
-    MB_ST = 15, MB_OT = 16, MB_RT = 17, MB_UT = 18, MB_DRAIN = 19, MB_GATE = 20, MB_GFREE = 22, MB_TBFREE = 24, MB_Q = 26, kNumBars = 27
+    MB_ST = 15, MB_OT = 16, MB_RT = 17, MB_UD = 18, MB_DRAIN = 19, MB_GATE = 20, MB_GFREE = 22, MB_TBFREE = 24, MB_Q = 26,
+    MB_UT = 27, kNumBars = 28
 };
 __device__ __forceinline__ uint32_t bar_count(int i) {
-    return (i >= MB_FREE && i < MB_KK) || (i >= MB_ST && i <= MB_UT) ? (uint32_t)kStateWarps : 1u;
+    return (i >= MB_FREE && i < MB_KK) || (i >= MB_ST && i <= MB_UD) || i == MB_UT ? (uint32_t)kStateWarps : 1u;
 }
+static_assert(kNumBars * 8 <= 224, "room for the barriers");
 constexpr uint32_t MISC_ABORT = 224, MISC_TMEM = 228, MISC_COUNT = 232;
 
-// TMEM columns.  16 columns of an fp32 row become 8 + 8 columns of its two terms.
-constexpr uint32_t COL_S = 0;              // S^T: term t of k-step s at 16 s + 8 t; dS
-constexpr uint32_t COL_PK = 128;           // Pk^T; U^T; its two terms as S
-constexpr uint32_t COL_PQ = 192;           // Pq^T
-constexpr uint32_t COL_R = 256;            // R^T, then U'^T: 3 terms x 32
-constexpr uint32_t COL_BU = 352;           // U^T B^T
+// TMEM columns.  16 columns of an fp32 row become 8 + 8 columns of its first two
+// terms; the third ones lie apart.
+constexpr uint32_t COL_S = 0;              // S^T: term t < 2 of k-step s at 16 s + 8 t; dS
+// Two tiles swap roles from chunk to chunk: X takes Pk^T, then two terms of R^T, then
+// U^T B^T; Y (the X of the chunk before, its O taken) U^T, then two terms of it.
+constexpr uint32_t COL_XY = 128;
+__device__ __forceinline__ uint32_t col_x(int chunk) { return COL_XY + 64u * (uint32_t)(chunk & 1); }
+__device__ __forceinline__ uint32_t col_y(int chunk) { return COL_XY + 64u * (uint32_t)(~chunk & 1); }
+constexpr uint32_t COL_PQ = 256;           // Pq^T
+constexpr uint32_t COL_S2 = 320;           // the third term of S^T, 8 s; then
+constexpr uint32_t COL_UD = 320;           // U'^T: 3 terms x 32
 constexpr uint32_t COL_KK = 416;           // [K ; Q] K^T of a chunk ahead
+constexpr uint32_t COL_RU2 = 480;          // the third term of R^T, then of U^T, 8 s
 constexpr uint32_t TMEM_COLS = 512;
 
 enum { BAR_PREP = 1 };                     // + group
@@ -197,26 +208,49 @@ __device__ __forceinline__ void split2(float2 v, uint32_t (&w)[N]) {
         if (i + 1 < N) v = __ffma2_rn(make_float2(bf_lo(w[i]), bf_hi(w[i])), make_float2(-1.f, -1.f), v);
     }
 }
-// 16 consecutive columns of an operand row as N terms at TMEM columns col,
-// col + stride, ...
-template <int N>
-__device__ __forceinline__ void put_split(uint32_t taddr, uint32_t stride, const float2 (&v)[8]) {
+// 16 consecutive columns of an operand row as three terms at TMEM columns, term by
+// term: eight words live at a time.
+// The leading 8 bits of both values, and what they leave.
+__device__ __forceinline__ uint32_t top2(float2 v) { return __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x7632u); }
+__device__ __forceinline__ float2 rest2(float2 v) {
+    return __ffma2_rn(make_float2(bf_hi(__float_as_uint(v.x)), bf_hi(__float_as_uint(v.y))), make_float2(-1.f, -1.f), v);
+}
+// Cut off one after another: exact.
+__device__ __forceinline__ void put_cut(uint32_t at0, uint32_t at1, uint32_t at2, const float2 (&v)[8]) {
+    float2 r[8];
+    uint32_t w[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+        w[u] = top2(v[u]);
+        r[u] = rest2(v[u]);
+    }
+    tmem_st8(at0, w);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+        w[u] = top2(r[u]);
+        r[u] = rest2(r[u]);
+    }
+    tmem_st8(at1, w);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) w[u] = top2(r[u]);
+    tmem_st8(at2, w);
+}
+// Rounded terms: two over the 16 columns themselves and a third at `third`.
+__device__ __forceinline__ void put_three(uint32_t taddr, uint32_t third, const float2 (&v)[8]) {
     float2 r[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u) r[u] = v[u];
 #pragma unroll
-    for (int i = 0; i < N; ++i) {          // term by term: eight words live at a time
+    for (int i = 0; i < 3; ++i) {
         uint32_t w[8];
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
             w[u] = pack_bf16x2(r[u].x, r[u].y);
-            if (i + 1 < N) r[u] = __ffma2_rn(make_float2(bf_lo(w[u]), bf_hi(w[u])), make_float2(-1.f, -1.f), r[u]);
+            if (i < 2) r[u] = __ffma2_rn(make_float2(bf_lo(w[u]), bf_hi(w[u])), make_float2(-1.f, -1.f), r[u]);
         }
-        tmem_st8(taddr + (uint32_t)i * stride, w);
+        tmem_st8(i < 2 ? taddr + 8u * (uint32_t)i : third, w);
     }
 }
-// The same as two terms over the 16 columns themselves.
-__device__ __forceinline__ void put_two(uint32_t taddr, const float2 (&v)[8]) { put_split<2>(taddr, 8, v); }
 __device__ __forceinline__ void get16(uint32_t taddr, float2 (&v)[8]) {
     float a[16];
     tmem_ld16(taddr, a);
@@ -341,10 +375,26 @@ struct Cursor {
     }
 };
 
+// A cursor of loads: with the first row and the head of its chunk at hand, so that
+// the issuing warp divides once a chain only (its next MMAs wait behind a load).
+struct Feed {
+    Cursor c;
+    int row, head, khead;
+    __device__ __forceinline__ void place(const PackedParams &p, const Sched &sc) {
+        if (!c.valid()) return;
+        row = sc.begin[c.seq(p, sc)];
+        head = c.head(p);
+        khead = head / p.group;
+    }
+    __device__ __forceinline__ void next(const PackedParams &p, const Sched &sc) {
+        row += C;
+        if (++c.n < c.chunks) return;
+        c.next_chain(p, sc);
+        place(p, sc);
+    }
+};
 // Loads of one chunk (one thread).
-__device__ __forceinline__ void request_kq(const PackedParams &p, const CUtensorMap *tm, const Ctx &x, const Sched &sc,
-                                           const Cursor &c, int stage) {
-    const int row = sc.begin[c.seq(p, sc)] + c.n * C, h = c.head(p) / p.group;
+__device__ __forceinline__ void request_kq(const CUtensorMap *tm, const Ctx &x, int row, int h, int stage) {
     const uint32_t kq = x.sbase + OFF_KQ + (uint32_t)stage * KQ_BYTES, mb = bar_addr(x, MB_KQ + stage);
     mbar_arrive_expect_tx(mb, KQ_BYTES);
     tma_load_3d(kq, &tm[0], 0, h, row, mb);
@@ -352,11 +402,10 @@ __device__ __forceinline__ void request_kq(const PackedParams &p, const CUtensor
     tma_load_3d(kq + 8192, &tm[1], 0, h, row, mb);
     tma_load_3d(kq + 16384 + 8192, &tm[1], 64, h, row, mb);
 }
-__device__ __forceinline__ void request_v(const PackedParams &p, const CUtensorMap *tm, const Ctx &x, const Sched &sc,
-                                          const Cursor &c) {
+__device__ __forceinline__ void request_v(const CUtensorMap *tm, const Ctx &x, int row, int h) {
     const uint32_t mb = bar_addr(x, MB_V);
     mbar_arrive_expect_tx(mb, 16384);
-    tma_load_3d(x.sbase + OFF_V, &tm[2], 0, c.head(p), sc.begin[c.seq(p, sc)] + c.n * C, mb);
+    tma_load_3d(x.sbase + OFF_V, &tm[2], 0, h, row, mb);
 }
 
 // =====================================================================
@@ -364,6 +413,26 @@ __device__ __forceinline__ void request_v(const PackedParams &p, const CUtensorM
 // =====================================================================
 __device__ __forceinline__ uint32_t tile_off(int r, int i) {      // 64 x 64 bf16, K-major, swizzled
     return (uint32_t)(r * 128 + (((i >> 3) ^ (r & 7)) << 4) + (i & 7) * 2);
+}
+// B has values in its lower 16 x 16 blocks only: k-step s (columns 16 s ..) is a strip
+// of the 4 - s blocks from rows 16 s on, an MMA of 64 - 16 s tokens.  The strips of all
+// three terms fill the room of two whole tiles: a strip stands in one of the four
+// 32-byte columns of the 128-byte rows, its first block b blocks of 16 rows down.
+//     column 0: (term 0, s 0), (1, 0)            column 1: (2, 0), (0, 1), (0, 3)
+//     column 2: (1, 1), (2, 1), (0, 2)           column 3: (1, 2), (2, 2), (1, 3), (2, 3)
+// 4 b + column of the strips s = 0 .. 3 of a term, a byte each.
+__host__ __device__ constexpr uint32_t strip_code(int term, int s) {
+    return ((term == 0 ? 0x1D1A1100u : term == 1 ? 0x13030210u : 0x170B0E01u) >> (8 * s)) & 31u;
+}
+// Offset of the strip's first row, and of 8 values of a row (16 bytes) in it.
+__device__ __forceinline__ uint32_t strip_off(int term, int s) {
+    const uint32_t c = strip_code(term, s);
+    return (c >> 2) * 2048u + (c & 3u) * 32u;
+}
+__device__ __forceinline__ uint32_t strip_at(int term, int r, int i) {
+    const int s = i >> 4;
+    const uint32_t c = strip_code(term, s);
+    return (c >> 2) * 2048u + (uint32_t)(r - 16 * s) * 128u + ((((c & 3u) * 2u + ((uint32_t)(i >> 3) & 1u)) ^ (uint32_t)(r & 7)) << 4);
 }
 // D (16 x 8 NB) = A (16 x 16) B (16 x 8 NB), fp32 tiles in shared memory, each
 // operand as tf32 head and tail: three products, the error of an fp32 product.
@@ -527,7 +596,7 @@ __device__ __forceinline__ void prep_page(const PackedParams &p, const Ctx &x, c
     }
     for (; cur.valid(); ++gc) {
         const int stage = gc % kStages, Cc = cur.rows();
-        uint8_t *aqk = sm + OFF_AQK + (uint32_t)stage * 2 * 8192;
+        uint8_t *aqk = sm + OFF_AQK + (uint32_t)stage * B_BYTES;
         float *vec = reinterpret_cast<float *>(sm + OFF_VEC + (uint32_t)stage * VEC_BYTES);
         cur.next(p, sc);                   // two on: the group's next chunk
         int step = 1;
@@ -616,13 +685,15 @@ __device__ __forceinline__ void prep_page(const PackedParams &p, const Ctx &x, c
                 if (is_q) {
 #pragma unroll
                     for (int j = 0; j < 16; j += 8) {
-                        uint32_t w[4][2];
+                        uint32_t w[4][3];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) split2<2>(make_float2(v[j + 2 * i], v[j + 2 * i + 1]), w[i]);
+                        for (int i = 0; i < 4; ++i) split2<3>(make_float2(v[j + 2 * i], v[j + 2 * i + 1]), w[i]);
+                        if (j0 <= row) {               // (no room for blocks above the diagonal)
 #pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            *reinterpret_cast<uint4 *>(aqk + i * 8192 + tile_off(row, j0 + j)) =
-                                make_uint4(w[0][i], w[1][i], w[2][i], w[3][i]);
+                            for (int i = 0; i < 3; ++i)
+                                *reinterpret_cast<uint4 *>(aqk + strip_at(i, row, j0 + j)) =
+                                    make_uint4(w[0][i], w[1][i], w[2][i], w[3][i]);
+                        }
                     }
                 } else {
 #pragma unroll
@@ -774,16 +845,17 @@ __device__ __forceinline__ void put_state(uint32_t tl, int hf, const float2 (&S)
         float2 v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = S[8 * q + i];
-        put_two(tl + COL_S + (uint32_t)(64 * hf + 16 * q), v);
+        const uint32_t at = tl + COL_S + (uint32_t)(64 * hf + 16 * q);
+        put_cut(at, at + 8u, tl + COL_S2 + (uint32_t)(32 * hf + 8 * q), v);
     }
 }
 
 // O^T = Pq^T Diag(fq) + U^T B^T of a chunk, as bf16 pairs of tokens.
-__device__ __forceinline__ void take_o(uint32_t tl, int hf, const float *fq, uint32_t (&o)[16]) {
+__device__ __forceinline__ void take_o(uint32_t tl, int chunk, int hf, const float *fq, uint32_t (&o)[16]) {
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
         float a[16], b[16];
-        tmem_ld16x2(tl + COL_PQ + (uint32_t)(32 * hf + 16 * q), tl + COL_BU + (uint32_t)(32 * hf + 16 * q), a, b);
+        tmem_ld16x2(tl + COL_PQ + (uint32_t)(32 * hf + 16 * q), tl + col_x(chunk) + (uint32_t)(32 * hf + 16 * q), a, b);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const float4 f = *reinterpret_cast<const float4 *>(fq + 16 * q + 4 * u);
@@ -850,7 +922,7 @@ __device__ __forceinline__ void state_page(const PackedParams &p, const Ctx &x, 
             uint32_t o[16];
             if (!wait_bar(x, bar_addr(x, MB_O), (uint32_t)((gc - 1) & 1))) return;
             fence_after_sync();
-            take_o(tl, hf, reinterpret_cast<const float *>(sm + OFF_VEC + (uint32_t)before * VEC_BYTES) + 64 + 32 * hf, o);
+            take_o(tl, gc - 1, hf, reinterpret_cast<const float *>(sm + OFF_VEC + (uint32_t)before * VEC_BYTES) + 64 + 32 * hf, o);
             fence_before_sync();
             __syncwarp();
             if (lane == 0) {
@@ -875,36 +947,44 @@ __device__ __forceinline__ void state_page(const PackedParams &p, const Ctx &x, 
             for (int u = 0; u < 8; ++u)
                 v[u] = make_float2(bf_lo(*reinterpret_cast<const uint16_t *>(vt + 4096 * q + 512 * u)),
                                    bf_lo(*reinterpret_cast<const uint16_t *>(vt + 4096 * q + 512 * u + 256)));
-            get16(tl + COL_PK + (uint32_t)(32 * hf + 16 * q), pk);
+            const uint32_t at = tl + col_x(gc) + (uint32_t)(32 * hf + 16 * q);
+            get16(at, pk);
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const float4 f = *reinterpret_cast<const float4 *>(vec + 16 * q + 4 * u);
                 v[2 * u] = __ffma2_rn(make_float2(f.x, f.y), pk[2 * u], v[2 * u]);
                 v[2 * u + 1] = __ffma2_rn(make_float2(f.z, f.w), pk[2 * u + 1], v[2 * u + 1]);
             }
-            put_split<3>(tl + COL_R + (uint32_t)(16 * hf + 8 * q), 32, v);
+            put_three(at, tl + COL_RU2 + (uint32_t)(16 * hf + 8 * q), v);
         }
         warp_arrive(x, MB_RT, lane);
         if (!wait_bar(x, bar_addr(x, MB_S), ph)) return;
         ph ^= 1u;
         fence_after_sync();
 #pragma unroll 1
-        for (int q = 0; q < 2; ++q) {      // U as two terms for O, Diag(c) U as three for dS
+        for (int q = 0; q < 2; ++q) {      // Diag(c) U for dS
             float2 v[8];
-            const uint32_t at = tl + COL_PK + (uint32_t)(32 * hf + 16 * q);
-            get16(at, v);
-            put_two(at, v);
+            get16(tl + col_y(gc) + (uint32_t)(32 * hf + 16 * q), v);
             scale16(v, vec + 128 + 16 * q);
-            put_split<3>(tl + COL_R + (uint32_t)(16 * hf + 8 * q), 32, v);
+            const uint32_t at = tl + COL_UD + (uint32_t)(16 * hf + 8 * q);
+            put_cut(at, at + 32u, at + 64u, v);
         }
         const float gamma = vec[192 - 32 * hf];
+        warp_arrive(x, MB_UD, lane);
+#pragma unroll 1
+        for (int q = 0; q < 2; ++q) {      // U for O, while dS is computed
+            float2 v[8];
+            const uint32_t at = tl + col_y(gc) + (uint32_t)(32 * hf + 16 * q);
+            get16(at, v);
+            put_three(at, tl + COL_RU2 + (uint32_t)(16 * hf + 8 * q), v);
+        }
         warp_arrive(x, MB_UT, lane);
         o_at = ch.o + (long long)cur.n * C * p.ldo;
         o_count = cur.rows() - 32 * hf;
         if (!wait_bar(x, bar_addr(x, MB_S), ph)) return;
         ph ^= 1u;
         fence_after_sync();
-        // S = gamma S + dS, and its terms over the columns of dS
+        // S = gamma S + dS, and its terms over the columns of dS and of the U' that made it
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             float2 v[8];
@@ -915,7 +995,7 @@ __device__ __forceinline__ void state_page(const PackedParams &p, const Ctx &x, 
                 S[8 * q + i] = __ffma2_rn(make_float2(gamma, gamma), S[8 * q + i], v[i]);
                 v[i] = S[8 * q + i];
             }
-            put_two(at, v);
+            put_cut(at, at + 8u, tl + COL_S2 + (uint32_t)(32 * hf + 8 * q), v);
         }
         const bool last = cur.n + 1 == cur.chunks;
         if (last) {
@@ -939,7 +1019,7 @@ __device__ __forceinline__ void state_page(const PackedParams &p, const Ctx &x, 
     if (!wait_bar(x, bar_addr(x, MB_O), (uint32_t)((gc - 1) & 1))) return;
     fence_after_sync();
     uint32_t o[16];                        // the last chunk's
-    take_o(tl, hf, reinterpret_cast<const float *>(sm + OFF_VEC + (uint32_t)((gc - 1) % kStages) * VEC_BYTES) + 64 + 32 * hf, o);
+    take_o(tl, gc - 1, hf, reinterpret_cast<const float *>(sm + OFF_VEC + (uint32_t)((gc - 1) % kStages) * VEC_BYTES) + 64 + 32 * hf, o);
     fence_before_sync();
     __syncwarp();
     if (lane == 0) mbar_arrive(bar_addr(x, MB_FREE + (gc - 1) % kStages));
@@ -954,6 +1034,9 @@ struct Issue {
     int kq_n, v_n, kk_n;                   // chunks of this CTA requested, and multiplied for the prep warps
     uint32_t ph;                           // phases of MB_S
 };
+
+// Column of term t of S^T for k-step s.
+__device__ __forceinline__ uint32_t s_col(int t, int s) { return t < 2 ? COL_S + 16u * s + 8u * t : COL_S2 + 8u * s; }
 
 // [K ; Q] K^T of chunk n, once its rows have landed and the product before it has been read.
 __device__ __forceinline__ bool issue_kk(const Ctx &x, Issue &is) {
@@ -979,22 +1062,25 @@ __device__ __forceinline__ void issue_page(const PackedParams &p, const CUtensor
     const uint32_t id_u = idesc_bf16(128, 64), id_s = idesc_bf16(128, 128, false, /*b_mn_major=*/true);
     const uint32_t tm = uniform(x.tm), mb = uniform(bar_addr(x, MB_S)), mo = uniform(bar_addr(x, MB_O));
     const uint32_t mt = uniform(bar_addr(x, MB_TBFREE)), mq = uniform(bar_addr(x, MB_Q)), tb = uniform(x.sbase + OFF_TB);
-    Cursor cur, kq, v;                     // the chunk at hand, the next K and Q, the next V to load
+    Cursor cur;                            // the chunk at hand
+    Feed kq, v;                            // the next K and Q, the next V to load
     cur.start(p, sc);
     if (!cur.valid()) return;
-    kq = v = cur;
+    kq.c = cur;
+    kq.place(p, sc);
+    v = kq;
     int left = 0;                          // chunks of the page whose product is not issued yet
     for (Cursor c = cur; c.valid(); c.next_chain(p, sc)) left += c.chunks;
     auto load_kq = [&]() {
-        if (!kq.valid()) return;
-        if (elect_one()) request_kq(p, tmaps, x, sc, kq, is.kq_n % kStages);
+        if (!kq.c.valid()) return;
+        if (elect_one()) request_kq(tmaps, x, kq.row, kq.khead, is.kq_n % kStages);
         __syncwarp();
         ++is.kq_n;
         kq.next(p, sc);
     };
     auto load_v = [&]() {
-        if (!v.valid()) return;
-        if (elect_one()) request_v(p, tmaps, x, sc, v);
+        if (!v.c.valid()) return;
+        if (elect_one()) request_v(tmaps, x, v.row, v.head);
         __syncwarp();
         ++is.v_n;
         v.next(p, sc);
@@ -1006,7 +1092,8 @@ __device__ __forceinline__ void issue_page(const PackedParams &p, const CUtensor
     for (bool first = true; cur.valid(); first = false, ++gc, cur.next(p, sc)) {
         const uint32_t par = (uint32_t)(gc & 1);
         const uint32_t a = uniform(x.sbase + OFF_KQ + (uint32_t)(gc % kStages) * KQ_BYTES);
-        const uint32_t aq = uniform(x.sbase + OFF_AQK + (uint32_t)(gc % kStages) * 2 * 8192);
+        const uint32_t aq = uniform(x.sbase + OFF_AQK + (uint32_t)(gc % kStages) * B_BYTES);
+        const uint32_t cx = uniform(x.tm + col_x(gc)), cy = uniform(x.tm + col_y(gc));
         // Pk^T = S^T K^T, small terms first; its columns still hold the U of the O before
         if (!wait_bar(x, bar_addr(x, MB_READY + (gc & 1)), (uint32_t)((gc >> 1) & 1))) return;
         if (!first && !wait_bar(x, bar_addr(x, MB_O), par ^ 1u)) return;
@@ -1015,11 +1102,10 @@ __device__ __forceinline__ void issue_page(const PackedParams &p, const CUtensor
         if (elect_one()) {
             fence_after_sync();
 #pragma unroll 1
-            for (int t = 1; t >= 0; --t)
+            for (int t = 2; t >= 0; --t)
 #pragma unroll
                 for (int s = 0; s < D / 16; ++s)
-                    mma_bf16_tmem_a(tm + COL_PK, tm + COL_S + (uint32_t)(16 * s + 8 * t), dk + kstep(128, s), id_u,
-                                    t < 1 || s > 0);
+                    mma_bf16_tmem_a(cx, tm + s_col(t, s), dk + kstep(128, s), id_u, t < 2 || s > 0);
             mma_commit(mb);
         }
         __syncwarp();
@@ -1029,11 +1115,10 @@ __device__ __forceinline__ void issue_page(const PackedParams &p, const CUtensor
         if (elect_one()) {
             fence_after_sync();
 #pragma unroll 1
-            for (int t = 1; t >= 0; --t)
+            for (int t = 2; t >= 0; --t)
 #pragma unroll
                 for (int s = 0; s < D / 16; ++s)
-                    mma_bf16_tmem_a(tm + COL_PQ, tm + COL_S + (uint32_t)(16 * s + 8 * t), dk + 512 + kstep(128, s), id_u,
-                                    t < 1 || s > 0);
+                    mma_bf16_tmem_a(tm + COL_PQ, tm + s_col(t, s), dk + 512 + kstep(128, s), id_u, t < 2 || s > 0);
             mma_commit(mq);
         }
         __syncwarp();
@@ -1050,10 +1135,10 @@ __device__ __forceinline__ void issue_page(const PackedParams &p, const CUtensor
 #pragma unroll 1
             for (int t = 0; t < 6; ++t) {
                 const uint32_t ra = (0x001012u >> (4 * t)) & 3u, ta = (0x010210u >> (4 * t)) & 3u;
+                const uint32_t r0 = ra < 2 ? cx + 8u * ra : tm + COL_RU2, rs = ra < 2 ? 16u : 8u;
 #pragma unroll
                 for (int s = 0; s < C / 16; ++s)
-                    mma_bf16_tmem_a(tm + COL_PK, tm + COL_R + 32u * ra + 8u * s, dt + ta * 512u + kstep(64, s), id_u,
-                                    t > 0 || s > 0);
+                    mma_bf16_tmem_a(cy, r0 + rs * s, dt + ta * 512u + kstep(64, s), id_u, t > 0 || s > 0);
             }
             mma_commit(mb);
             mma_commit(mt + 8u * par);
@@ -1062,25 +1147,32 @@ __device__ __forceinline__ void issue_page(const PackedParams &p, const CUtensor
         is.ph ^= 1u;
         load_v();                          // every state warp has read this chunk's
         // dS^T = U'^T K over the columns of S, then U^T B^T
-        if (!wait_bar(x, bar_addr(x, MB_UT), par)) return;
+        if (!wait_bar(x, bar_addr(x, MB_UD), par)) return;
         if (!wait_bar(x, bar_addr(x, MB_Q), par)) return;
         if (elect_one()) {
             fence_after_sync();
-            const uint64_t dm = mn_desc(a, 16384, 0), da = kmaj_desc(aq, 64, 0);
+            const uint64_t dm = mn_desc(a, 16384, 0);
 #pragma unroll 1
             for (int t = 2; t >= 0; --t)
 #pragma unroll
                 for (int s = 0; s < C / 16; ++s)
-                    mma_bf16_tmem_a(tm + COL_S, tm + COL_R + 32u * t + 8u * s, dm + mnstep(s), id_s, t < 2 || s > 0);
+                    mma_bf16_tmem_a(tm + COL_S, tm + COL_UD + 32u * t + 8u * s, dm + mnstep(s), id_s, t < 2 || s > 0);
             mma_commit(mb);
-            // terms (1,0), (0,1), (0,0) of U and B
+        }
+        __syncwarp();
+        if (!wait_bar(x, bar_addr(x, MB_UT), par)) return;
+        if (elect_one()) {
+            fence_after_sync();
+            const uint64_t da = kmaj_desc(aq, 64, 0);
+            // terms (2,0), (1,1), (0,2), (1,0), (0,1), (0,0) of U and B, B by strips
 #pragma unroll 1
-            for (int t = 0; t < 3; ++t) {
-                const uint32_t ua = t == 0, ba = t == 1;
+            for (int t = 0; t < 6; ++t) {
+                const int ua = (0x001012 >> (4 * t)) & 3, ba = (0x010210 >> (4 * t)) & 3;
+                const uint32_t u0 = ua < 2 ? cy + 8u * (uint32_t)ua : tm + COL_RU2, us = ua < 2 ? 16u : 8u;
 #pragma unroll
                 for (int s = 0; s < C / 16; ++s)
-                    mma_bf16_tmem_a(tm + COL_BU, tm + COL_PK + 16u * s + 8u * ua, da + ba * 512u + kstep(64, s), id_u,
-                                    t > 0 || s > 0);
+                    mma_bf16_tmem_a(cx + 16u * s, u0 + us * s, da + (strip_off(ba, s) >> 4),
+                                    idesc_bf16(128, 64 - 16 * s), t > 0 || s > 0);
             }
             mma_commit(mo);
         }
@@ -1112,8 +1204,8 @@ packed_chunk_kernel(const __grid_constant__ PackedTcParams tp) {
         *x.abort_flag = 0;
         fence_mbar_init();
     }
-    // what lies above the diagonal of T Diag(beta) and B is never written again
-    for (uint32_t i = tid; i < (OFF_A - OFF_TB) / 16; i += kThreads)
+    // what lies above the diagonal blocks of T Diag(beta) is never written again
+    for (uint32_t i = tid; i < (OFF_AQK - OFF_TB) / 16; i += kThreads)
         *reinterpret_cast<uint4 *>(sm + OFF_TB + 16 * i) = make_uint4(0, 0, 0, 0);
     fence_async_smem();
     fence_before_sync();

@@ -340,8 +340,8 @@ kda_status kda_output_gate(const kda_gate_args *args, void *stream);
  * algo: KDA_ALGO_SIMT runs the recurrence token by token in fp32 (any width,
  * dtype and decay); KDA_ALGO_TC the chunk form on the tensor cores (bf16,
  * Dk = Dv = 128, g_per_head, any decay, 16-byte aligned rows; fp32 operands
- * enter as two or three bf16 terms each, so the state stays within about 1e-6 of
- * an fp32 one), KDA_ERR_UNSUPPORTED or KDA_ERR_ALIGNMENT otherwise.
+ * enter as three bf16 terms each, so the state is as exact as the recurrence's),
+ * KDA_ERR_UNSUPPORTED or KDA_ERR_ALIGNMENT otherwise.
  * KDA_ALGO_AUTO takes the chunk form for sequences longer than 12 rows where it
  * applies and the recurrence for all others; both kernels then run, each on its
  * sequences.  In the chunk form a NaN or infinity in q, k, v, g or beta reaches

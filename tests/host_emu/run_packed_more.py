@@ -1,0 +1,80 @@
+"""More host-emulated runs of the packed kernels -- TEST INFRASTRUCTURE, started by
+tests/test_packed_emu_more_cpu.py in a process with a sanitizer's runtime
+preloaded: ``run_packed_more.py NAME [LIB]`` runs the function of that name and
+exits non-zero if it fails.
+"""
+import ctypes
+import os
+import sys
+
+import numpy as np
+import torch
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+sys.path.insert(0, HERE)
+sys.path.insert(0, os.path.dirname(HERE))
+sys.path.insert(0, os.path.dirname(os.path.dirname(HERE)))
+import run_packed as rp  # noqa: E402
+from helpers import to_np  # noqa: E402
+from oracle import packed  # noqa: E402
+
+
+def fp32_recurrence(q, k, v, g, beta, S, scale):
+    """One chain token by token in 32 bits (q, k normalised in 64), o and S."""
+    f = np.float32
+    o = np.empty_like(v, dtype=f)
+    S = S.astype(f)
+    q = (q / np.sqrt((q * q).sum(-1, keepdims=True) + 1e-6) * scale).astype(f)
+    k = (k / np.sqrt((k * k).sum(-1, keepdims=True) + 1e-6)).astype(f)
+    v, a, b = v.astype(f), np.exp(g).astype(f), (1 / (1 + np.exp(-beta))).astype(f)
+    for t in range(len(v)):
+        S = S * a[t]
+        S = S + np.outer(k[t], b[t] * (v[t] - k[t] @ S))
+        o[t] = q[t] @ S
+    return o, S
+
+
+def precision(lib):
+    """The chunk form of one chain with hardly any decay, where errors of the state
+    stay longest: no further from 64 bits than a recurrence in 32 bits, in the
+    state and in the share of bf16 outputs that are not the rounded exact ones."""
+    T, bf = 256, torch.bfloat16
+    for seed, z_mean in ((1, -8.0), (2, -4.0)):
+        gen = torch.Generator().manual_seed(seed)
+        q, k, v = (torch.randn(T, 1, 128, generator=gen).to(bf) for _ in range(3))
+        g, beta = (torch.randn(T, 1, generator=gen) + z_mean).to(bf), torch.randn(T, 1, generator=gen).to(bf)
+        A, b = torch.zeros(1), torch.zeros(1)
+        pool, o = torch.randn(1, 1, 128, 128, generator=gen) * 0.05, torch.zeros(T, 1, 128, dtype=bf)
+        scale = 128 ** -0.5
+        want_o, want_S = packed.packed_fwd(*map(to_np, (q, k, v, g, beta, pool, o)), cu=[0, T], A_log=to_np(A),
+                                           dt_bias=to_np(b), gate="softplus", per_head=True, scale=scale)
+        decay = packed.log_decay(to_np(g), to_np(A), to_np(b), "softplus", True, 1)[:, 0, 0]
+        rec_o, rec_S = fp32_recurrence(*(to_np(t)[:, 0] for t in (q, k, v)), decay, to_np(beta)[:, 0],
+                                       to_np(pool)[0, 0], scale)
+        cu = torch.tensor([0, T], dtype=torch.int32)
+        p = rp.PackedParams(1, T, 1, 1, 1, 128, 128, 1, -5.0, scale, 1e-6, 1, 1, 2, 1, 0,
+                            *(t.stride(0) for t in (q, k, v, g, beta, o)),
+                            *map(rp._ptr, (q, k, v, g, beta, A, b, cu, None, None, pool, o)))
+        lib.emu_packed_chunk(ctypes.byref(p), 1)
+
+        def off(S):
+            return np.linalg.norm(to_np(S) - want_S[0, 0]) / np.linalg.norm(want_S)
+
+        rounded = torch.from_numpy(want_o[:, 0]).to(bf)
+        flips = [int((x != rounded).sum()) for x in (o[:, 0], torch.from_numpy(rec_o).to(bf))]
+        errs = [off(pool[0, 0]), off(torch.from_numpy(rec_S))]
+        print("state off by %.2e (32 bits: %.2e), outputs %d (%d) of %d" % (*errs, *flips, rounded.numel()), flush=True)
+        assert errs[0] <= errs[1]
+        # counts of rare events: three standard deviations of the recurrence's own count
+        assert flips[0] <= flips[1] + 3 * flips[1] ** 0.5 + 3
+
+
+def main():
+    import emu_packed
+    lib = rp.load(sys.argv[2] if len(sys.argv) > 2 else emu_packed.LIB)
+    globals()[sys.argv[1]](lib)
+    print("done")
+
+
+if __name__ == "__main__":
+    main()
