@@ -69,6 +69,29 @@ def precision(lib):
         assert flips[0] <= flips[1] + 3 * flips[1] ** 0.5 + 3
 
 
+# Chunk-kernel runs that come round: several chunks a chain, chains and sequences one
+# after another, so that every stage, parity and buffer is used again.
+ONE = dict(cu=[0, 400], slots=[0], fresh=None, P=1)
+LAST = dict(cu=[0, 150, 150, 341], slots=[1, 0, 2], fresh=[0, 0, 1], P=3)
+ROUNDS = [
+    dict(pack=rp.LONG, T=230, H=1, HV=2, ctas=2), dict(pack=ONE, T=400, H=1, HV=1, ctas=1),
+    dict(pack=LAST, T=341, H=1, HV=2, ctas=1),
+]
+
+
+def chunk_rounds(lib):
+    for i, kw in enumerate(ROUNDS):
+        errs = rp.run_delta(lib, Dk=128, Dv=128, dtype="bf16", gate="softplus", per_head=True, seed=20 + i, **kw)
+        print({n: "%.1e" % e for n, (e, _) in errs.items()}, flush=True)
+        assert all(e <= tol for e, tol in errs.values())
+
+
+def chunk_rounds_races(lib):
+    """For the thread sanitizer: no oracle."""
+    for kw in ROUNDS:
+        rp.run_delta(lib, Dk=128, Dv=128, dtype="bf16", gate="softplus", per_head=True, check=False, **kw)
+
+
 def main():
     import emu_packed
     lib = rp.load(sys.argv[2] if len(sys.argv) > 2 else emu_packed.LIB)

@@ -26,3 +26,14 @@ def _run(name, sanitizer="address"):
 
 def test_chunk_form_is_as_exact_as_a_recurrence_in_32_bits():
     _run("precision")
+
+
+def test_chunk_form_comes_round():
+    _run("chunk_rounds")
+
+
+def test_chunk_form_comes_round_without_data_races():
+    """Every wait that guards a buffer used again: stages of K and Q, B and the row
+    factors, T, V, the products for the prep warps, the state from chunk to chunk."""
+    r = _run("chunk_rounds_races", "thread")
+    assert "data race" not in r.stderr, r.stderr[-4000:]
