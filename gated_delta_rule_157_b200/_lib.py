@@ -550,9 +550,9 @@ def kda_packed_fwd(q, k, v, g, beta, pool, *, cu_seqlens=None, slots=None, fresh
     "auto", "simt" (recurrence, fp32) or "tc" (chunks on the tensor cores: bf16,
     Dk = Dv = 128, g_per_head).  The other arguments as kda_chunk_fwd.
 
-    The arrays are read on the device: bounds outside [0, T], a slot >= P or one
-    that an earlier sequence names make the sequence skipped and reported by
-    kda_device_status.
+    The arrays are read on the device: bounds outside [0, T], a slot >= P or (both
+    with rows) one that an earlier sequence names make the sequence skipped and
+    reported by kda_device_status.
     """
     lib = load()
     if not isinstance(q, torch.Tensor) or not q.is_cuda:

@@ -175,8 +175,8 @@ packed_recurrent_kernel(const PackedParams p) {
         }
     }
 
-    const bool repeat = __syncthreads_or(packed_repeat(p.slots, s, sq.slot, tid, blockDim.x));
-    if ((sq.bad || repeat) && tid == 0 && hv == 0 && blockIdx.y == 0) atomicOr(&g_packed_error, kPackedRange);
+    const bool repeat = __syncthreads_or(packed_repeat(p.cu, p.slots, s, sq.slot, tid, blockDim.x));
+    if ((sq.bad || (repeat && sq.len > 0)) && tid == 0 && hv == 0 && blockIdx.y == 0) atomicOr(&g_packed_error, kPackedRange);
     if (!mine || repeat) return;
     const float ea = expf(A);
     for (int t0 = 0, buf = 0; t0 < sq.len; t0 += tile, buf ^= 1) {

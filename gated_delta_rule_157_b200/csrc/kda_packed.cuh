@@ -35,7 +35,7 @@ struct PackedConvParams {
 };
 
 // Error word bit: a sequence with row bounds outside [0, T], a slot outside the
-// pool, or a slot that an earlier sequence of the call has: skipped.
+// pool, or (both with rows) a slot that an earlier sequence of the call has: skipped.
 constexpr unsigned kPackedRange = 2u;
 
 struct PackedSeq {
@@ -53,9 +53,11 @@ __device__ __forceinline__ PackedSeq packed_seq(const int *cu, const int *slots,
     return r;
 }
 
-// Whether an earlier sequence names the same slot: this thread's share of the
-// search (threads tid, tid + step, ...); the caller ORs over the threads.
-__device__ __forceinline__ bool packed_repeat(const int *slots, int s, int slot, int tid, int step) {
+// Whether an earlier sequence names the same slot (one without rows does not count):
+// this thread's share of the search (threads tid, tid + step, ...); the caller ORs
+// over the threads.
+__device__ __forceinline__ bool packed_has_rows(const int *cu, int s) { return !cu || cu[s + 1] != cu[s]; }
+__device__ __forceinline__ bool packed_repeat(const int *cu, const int *slots, int s, int slot, int tid, int step) {
     bool hit = false;
     if (slots && slot >= 0)
         for (int i = tid; i < s; i += 8 * step) {
@@ -63,7 +65,8 @@ __device__ __forceinline__ bool packed_repeat(const int *slots, int s, int slot,
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[k] = i + k * step < s ? slots[i + k * step] : -1;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) hit |= v[k] == slot;
+            for (int k = 0; k < 8; ++k)
+                if (v[k] == slot) hit |= packed_has_rows(cu, i + k * step);
         }
     return hit;
 }

@@ -162,7 +162,7 @@ packed_conv_kernel(const PackedConvParams p, int run) {
             if (c_ok && row + u < end) ahead[u].load(x + (long long)(row + u) * p.ldx);
         }
         const bool zero = p.fresh && p.fresh[s];
-        const bool repeat = __any_sync(0xffffffffu, packed_repeat(p.slots, s, sq.slot, lane, 32));
+        const bool repeat = __any_sync(0xffffffffu, packed_repeat(p.cu, p.slots, s, sq.slot, lane, 32));
         if (repeat) {
             if (row == b && lane == 0) atomicOr(&g_packed_conv_error, kPackedRange);
             continue;

@@ -319,8 +319,9 @@ __device__ void fill_page(const PackedParams &p, const Sched &sc, int s0, int ti
     for (int i = tid; i < n; i += kThreads) {
         bool live = sc.len[i] > p.split && sc.slot[i] >= 0;
         if (live && p.slots) {             // (the recurrence looks at the short ones)
-            bool repeat = packed_repeat(p.slots, s0, sc.slot[i], 0, 1);
-            for (int k = 0; k < i; ++k) repeat |= sc.slot[k] == sc.slot[i];
+            bool repeat = packed_repeat(p.cu, p.slots, s0, sc.slot[i], 0, 1);
+            for (int k = 0; k < i; ++k)
+                if (sc.slot[k] == sc.slot[i]) repeat |= packed_has_rows(p.cu, s0 + k);
             if (repeat && blockIdx.x == 0) atomicOr(&g_packed_chunk_error, kPackedRange);
             live = live && !repeat;
         }

@@ -325,10 +325,10 @@ kda_status kda_output_gate(const kda_gate_args *args, void *stream);
  *
  * These arrays live on the device and are read by the kernels, so a captured
  * call replays with whatever they then hold.  A sequence of no rows changes
- * nothing, its slot included.  A sequence whose bounds lie outside [0, T], whose
- * slot is >= P, or (with rows) whose slot an earlier sequence of the call also
- * names, is skipped like a negative slot and reported by kda_device_status as
- * KDA_ERR_RANGE.  Output rows that two sequences share (overlapping bounds)
+ * nothing, its slot included, and its slot may be another's.  A sequence whose
+ * bounds lie outside [0, T], whose slot is >= P, or (with rows) whose slot an earlier
+ * sequence with rows also names, is skipped like a negative slot and reported by
+ * kda_device_status as KDA_ERR_RANGE.  Output rows that two sequences share (overlapping bounds)
  * hold one of the two results.
  * ------------------------------------------------------------------------- */
 

@@ -7,7 +7,7 @@
   * ``group_norm`` / ``group_norm_backward`` -- the formulas in NumPy.
 
 A sequence is live if it has rows, its bounds lie in [0, T], its slot is in the
-pool and no earlier sequence names that slot.
+pool and no earlier sequence with rows names that slot.
 """
 import numpy as np
 
@@ -28,8 +28,9 @@ def live(cu, slots, T, P, n):
         slot = s if slots is None else int(slots[s])
         bad = b < 0 or e < b or e > T or slot >= P
         repeat = slots is not None and slot >= 0 and slot in seen
-        seen.add(slot)
-        report |= bad or repeat
+        if e != b:
+            seen.add(slot)
+        report |= bad or (repeat and e > b)
         if not bad and not repeat and slot >= 0 and e > b:
             out.append((s, b, e, slot))
     return out, report

@@ -92,6 +92,22 @@ def chunk_rounds_races(lib):
         rp.run_delta(lib, Dk=128, Dv=128, dtype="bf16", gate="softplus", per_head=True, check=False, **kw)
 
 
+# Sequences without rows that name another's slot, behind it, ahead of it and among
+# themselves: legal, nothing is reported and nobody is skipped.
+SHARED = dict(cu=[0, 0, 3, 3, 70, 70, 70], slots=[1, 0, 0, 1, 2, 2], fresh=None, P=3)
+
+
+def empty_sequences(lib):
+    runs = [(rp.run_delta, dict(H=1, HV=1, Dk=24, Dv=8, dtype="f32", gate="bounded", per_head=False)),
+            (rp.run_delta, dict(H=1, HV=1, Dk=128, Dv=128, dtype="bf16", gate="softplus", per_head=True, ctas=1)),
+            (rp.run_conv, dict(C=128, K=4, dtype="f32", head_dim=0, silu=True, run=4))]
+    assert not packed.live(SHARED["cu"], SHARED["slots"], 70, 3, 6)[1]
+    for i, (fn, kw) in enumerate(runs):
+        errs = fn(lib, pack=SHARED, T=70, seed=40 + i, **kw)
+        print(fn.__name__, {n: "%.1e" % e for n, (e, _) in errs.items()}, flush=True)
+        assert all(e <= tol for e, tol in errs.values())
+
+
 def main():
     import emu_packed
     lib = rp.load(sys.argv[2] if len(sys.argv) > 2 else emu_packed.LIB)

@@ -1,0 +1,29 @@
+"""Packed batches on the GPU at their edges: sequences without rows that share a slot,
+outputs that the call allocates, bounds that are not what they should be."""
+import numpy as np
+import pytest
+import torch
+
+import gated_delta_rule_157_b200 as kda
+from helpers import to_np
+from test_packed_gpu import batch, check, close, conv_batch, conv_expect
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("per_head,algo", [(False, "auto"), (True, "auto"), (True, "tc"), (True, "simt")])
+def test_empty_sequences_may_name_anothers_slot(cuda_device, per_head, algo):
+    """A batch padded with empty sequences, ahead of and behind the ones whose slots
+    they name: nobody is skipped, nothing is reported."""
+    t, kw = batch(cuda_device, [0, 3, 0, 67, 0, 0], 1, 2, 128, 128, "bf16", "softplus", per_head, P=4,
+                  slots=[1, 0, 0, 1, 2, 2])
+    check(t, kw, algo=algo)            # ends with kda_device_status
+
+
+def test_empty_sequences_in_the_convolution(cuda_device):
+    t, kw = conv_batch(cuda_device, [0, 3, 0, 67, 0, 0], 128, 4, "bf16", slots=[1, 0, 0, 1, 2, 2], P=4)
+    y, pool = conv_expect(t, kw)
+    kda.kda_packed_conv(t["x"], t["w"], t["pool"], t["bias"], y=t["y"], **kw)
+    close(t["y"], y)
+    assert np.array_equal(to_np(t["pool"]), pool)
+    kda.kda_device_status()

@@ -37,3 +37,7 @@ def test_chunk_form_comes_round_without_data_races():
     factors, T, V, the products for the prep warps, the state from chunk to chunk."""
     r = _run("chunk_rounds_races", "thread")
     assert "data race" not in r.stderr, r.stderr[-4000:]
+
+
+def test_empty_sequences_may_name_anothers_slot():
+    _run("empty_sequences")
