@@ -75,18 +75,30 @@ template <> struct Raw8<float> {
 __device__ __forceinline__ float silu_for(const float *, float u) { return u / (1.f + expf(-u)); }
 __device__ __forceinline__ float silu_for(const __nv_bfloat16 *, float u) { return u * rcpf_(1.f + ex2f_(-kLog2E * u)); }
 
-// The last sequence that begins at or before `row` (0 if none does): 32 bounds at a time.
-__device__ __forceinline__ int find_sequence(const int *cu, int n, int row, int lane) {
-    int lo = 0, len = n;                   // the answer is in [lo, lo + len)
-    while (len > 1) {
-        const int step = (len + 31) / 32, at = lo + lane * step;
-        const bool le = lane * step < len && cu[at] <= row;
-        const int k = __popc(__ballot_sync(0xffffffffu, le)) - 1;     // bounds do not decrease
-        if (k < 0) return 0;
-        lo += k * step;
-        len = min(step, len - k * step);
+// Where to begin looking for the sequences of `row` and of those behind it: the last
+// that begins at or before it.  Where bounds run backwards that is no answer: all
+// sequences are looked at then.  (Eight bounds a lane in one round; whatever a warp
+// does for a sequence reads all slots once, so reading all bounds once costs little.)
+__device__ __forceinline__ int find_sequence(const int *cu, int n, int row, int lane, bool &backwards) {
+    int count = 0;
+    bool down = false;
+    for (int i0 = 0; i0 < n; i0 += 256) {
+        int a[8], b[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int i = i0 + 32 * k + lane;
+            a[k] = i < n ? cu[i] : 0x7FFFFFFF;
+            b[k] = i < n ? cu[i + 1] : 0x7FFFFFFF;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (i0 + 32 * k < n) {
+                count += __popc(__ballot_sync(0xffffffffu, a[k] <= row));
+                down |= b[k] < a[k];
+            }
     }
-    return lo;
+    backwards = __any_sync(0xffffffffu, down);
+    return backwards || count == 0 ? 0 : count - 1;
 }
 
 // kAhead: rows done together, and requested ahead: 4, or 1 where runs are single rows.
@@ -145,11 +157,15 @@ packed_conv_kernel(const PackedConvParams p, int run) {
         }
     }
 
-    for (int s = p.cu ? find_sequence(p.cu, p.N, r0, lane) : r0; s < p.N; ++s) {
+    bool backwards = false;
+    for (int s = p.cu ? find_sequence(p.cu, p.N, r0, lane, backwards) : r0; s < p.N; ++s) {
         const PackedSeq sq = packed_seq(p.cu, p.slots, p.T, p.P, s);
         if (sq.bad || sq.len == 0) continue;
         const int b = sq.begin, e = b + sq.len;
-        if (b >= r1) break;
+        if (b >= r1) {
+            if (backwards) continue;
+            break;
+        }
         int row = b > r0 ? b : r0;
         if (row > b && row < b + W) row = b + W < e ? b + W : e;      // the run with row b does these
         const int own = b >= r0 && b + W > r1 ? b + W : r1;

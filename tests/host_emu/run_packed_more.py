@@ -108,6 +108,38 @@ def empty_sequences(lib):
         assert all(e <= tol for e, tol in errs.values())
 
 
+def conv_bounds(lib):
+    """The convolution over bounds of which some lie outside the rows or run backwards:
+    every sequence whose own bounds are good is computed, whatever the others hold."""
+    rng = np.random.default_rng(5)
+    packs = [[0, 5, -3, 12], [0, 6, 40, 41, 9, 12], [-2, 4, 4, 9, 100, 12]]
+    for n in (5, 40, 40, 70):
+        cu = np.sort(rng.integers(0, 151, n + 1))
+        bad = rng.choice(n + 1, 3, replace=False)
+        packs.append(np.where(np.isin(np.arange(n + 1), bad), rng.choice([-7, 160, 1 << 30, 3], n + 1), cu).tolist())
+    for i, cu in enumerate(packs):
+        T, n = max(x for x in cu if x <= 151), len(cu) - 1
+        pack = dict(cu=cu, slots=list(range(n)), fresh=None, P=n)
+        gen = torch.Generator().manual_seed(i)
+        for dtype, run in ((torch.float32, 1), (torch.bfloat16, 4), (torch.float32, 8)):
+            C, K = 128, 4
+            x, w = torch.randn(T, C, generator=gen).to(dtype), torch.randn(C, K, generator=gen)
+            pool, y = torch.randn(n, K - 1, C, generator=gen).to(dtype), torch.full((T, C), 0.0625).to(dtype)
+            want_y, want_pool = packed.packed_conv(*map(to_np, (x, w, pool, y)), cu=cu, slots=pack["slots"], silu=False)
+            live, report = packed.live(cu, pack["slots"], T, n, n)
+            once = np.zeros(T, dtype=int)             # rows of two sequences hold either's result
+            for _, b, e, _ in live:
+                once[b:e] += 1
+            n_, cut, slots, _ = rp.pack_of(pack, T)
+            p = rp.ConvParams(n, T, n, C, K, 0, 0, 1e-6, C, C, *map(rp._ptr, (x, w, None, cut, slots, None, pool, y)))
+            word = lib.emu_packed_conv(ctypes.byref(p), int(dtype == torch.bfloat16), run)
+            assert bool(word) == report and report, cu
+            assert np.array_equal(to_np(pool), want_pool), (cu, run)
+            tol = rp.TOL["bf16" if dtype == torch.bfloat16 else "f32"]
+            err = np.abs(to_np(y) - want_y)[once < 2].max() / np.abs(want_y).max()
+            assert err <= tol, (cu, run, err)
+
+
 def main():
     import emu_packed
     lib = rp.load(sys.argv[2] if len(sys.argv) > 2 else emu_packed.LIB)

@@ -27,3 +27,20 @@ def test_empty_sequences_in_the_convolution(cuda_device):
     close(t["y"], y)
     assert np.array_equal(to_np(t["pool"]), pool)
     kda.kda_device_status()
+
+
+@pytest.mark.parametrize("cu", [[0, 5, 3, 60, 200, 210, 172], [-4, 2, 40, 41, 41, 42, 43], [0, 90, -3, 150, 160, 165, 172]])
+def test_convolution_skips_bad_bounds_only(cuda_device, cu):
+    """Bounds that run backwards or leave the rows: reported, and every sequence whose
+    own bounds are good is computed."""
+    t, kw = conv_batch(cuda_device, [3, 70, 4, 50, 2, 40], 256, 4, "bf16", slots=[4, 1, 0, 2, 3, 8], P=9, behind=3)
+    kw["cu_seqlens"] = torch.tensor(cu, dtype=torch.int32, device=cuda_device)
+    y, pool = conv_expect(t, kw)
+    kda.kda_packed_conv(t["x"], t["w"], t["pool"], t["bias"], y=t["y"], **kw)
+    assert np.array_equal(to_np(t["pool"]), pool)
+    once = torch.ones(172, dtype=torch.bool)
+    if cu[1] == 5:                         # rows 3 and 4 are sequence 0's and sequence 2's: either's result
+        once[3:5] = False
+    close(t["y"][once.to(cuda_device)], y[once.numpy()])
+    with pytest.raises(kda.KdaError):
+        kda.kda_device_status()

@@ -41,3 +41,7 @@ def test_chunk_form_comes_round_without_data_races():
 
 def test_empty_sequences_may_name_anothers_slot():
     _run("empty_sequences")
+
+
+def test_convolution_skips_bad_bounds_only():
+    _run("conv_bounds")
