@@ -2,9 +2,11 @@
 
 KDAChunkFunction runs kda_chunk_fwd keeping the per-chunk states, and
 kda_chunk_bwd in its backward.  Marshalling only: both passes run
-in the library's kernels.
+in the library's kernels.  The gradients have no gradient of their own: a second
+derivative through either function is an error.
 """
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 
@@ -26,6 +28,7 @@ class KDAChunkFunction(torch.autograd.Function):
         return o, S_T
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, do, dS_T):
         q, k, v, g, beta, A_log, dt_bias, S_chunks = ctx.saved_tensors
         if do is None:
@@ -65,6 +68,7 @@ class KDAGroupNormFunction(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, weight, bias, gate, mean, rstd = ctx.saved_tensors
         need = ctx.needs_input_grad
