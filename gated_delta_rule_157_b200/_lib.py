@@ -532,6 +532,12 @@ def _check_packing(cu_seqlens, slots, fresh, rows, dev):
     return n, fresh
 
 
+def _check_no_grad(name, *tensors):
+    """For entry points without a backward: gradients would be lost in silence."""
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        raise ValueError("%s has no backward: call it under torch.no_grad() or on detached tensors" % name)
+
+
 @_on_stream
 def kda_packed_fwd(q, k, v, g, beta, pool, *, cu_seqlens=None, slots=None, fresh=None, max_seqlen=None,
                    A_log=None, dt_bias=None, g_min=-5.0, scale=1.0, l2_eps=1e-6, qk_l2norm_in_kernel=True,
@@ -552,7 +558,8 @@ def kda_packed_fwd(q, k, v, g, beta, pool, *, cu_seqlens=None, slots=None, fresh
 
     The arrays are read on the device: bounds outside [0, T], a slot >= P or (both
     with rows) one that an earlier sequence names make the sequence skipped and
-    reported by kda_device_status.
+    reported by kda_device_status.  No backward: under grad mode, tensors that
+    require grad are refused (training takes kda_chunk).
     """
     lib = load()
     if not isinstance(q, torch.Tensor) or not q.is_cuda:
@@ -575,6 +582,7 @@ def kda_packed_fwd(q, k, v, g, beta, pool, *, cu_seqlens=None, slots=None, fresh
     if o is None:
         o = torch.empty((T, HV, Dv), dtype=dt, device=dev)
     ld_o = _check_rows(o, "o", (T, HV, Dv), dt, dev)
+    _check_no_grad("kda_packed_fwd", q, k, v, g, beta, A_log, dt_bias, pool, o)
     a = PackedArgs(n, T, P, H, HV, Dk, Dv, int(max_seqlen or 0), code, ALGOS[algo], g_min, scale, l2_eps,
                    bool(qk_l2norm_in_kernel), bool(beta_sigmoid_in_kernel), _gate_code(gate_in_kernel), per_head,
                    ld_q, ld_k, ld_v, ld_g, ld_b, ld_o, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
@@ -590,7 +598,7 @@ def kda_packed_conv(x, w, pool, bias=None, *, cu_seqlens=None, slots=None, fresh
     """kda_short_conv over a packed batch: x [T,C] float32 or bfloat16 (C % 128
     == 0, rows may lie apart), w [C,K], bias [C] float32; pool [P,K-1,C] of x's
     type holds each slot's window and is updated in place.  cu_seqlens, slots
-    and fresh as kda_packed_fwd.  Returns y [T,C]."""
+    and fresh as kda_packed_fwd.  Returns y [T,C].  No backward, as there."""
     lib = load()
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise ValueError("x must be a CUDA tensor")
@@ -606,6 +614,7 @@ def kda_packed_conv(x, w, pool, bias=None, *, cu_seqlens=None, slots=None, fresh
     if y is None:
         y = torch.empty((T, C), dtype=dt, device=dev)
     ld_y = _check_rows(y, "y", (T, C), dt, dev)
+    _check_no_grad("kda_packed_conv", x, w, bias, pool, y)
     a = PackedConvArgs(n, T, P, C, K, int(head_dim), bool(silu), code, l2_eps, ld_x, ld_y, x.data_ptr(), w.data_ptr(),
                        _ptr(bias), _ptr(cu_seqlens), _ptr(slots), _ptr(fresh), _ptr(pool), y.data_ptr())
     _launch("kda_packed_conv", dev, lib.kda_packed_conv, a, stream)

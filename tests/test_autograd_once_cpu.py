@@ -56,3 +56,12 @@ def test_chunk_gradient_has_no_gradient(monkeypatch):
     (dv,) = torch.autograd.grad((o ** 3).sum(), v, create_graph=True)
     with pytest.raises(RuntimeError, match="once_differentiable"):
         (dv ** 2).sum().backward()
+
+
+def test_packed_calls_refuse_what_needs_a_gradient():
+    a, b = torch.zeros(2), torch.zeros(2, requires_grad=True)
+    _lib._check_no_grad("call", a, None, a)
+    with pytest.raises(ValueError, match="no backward"):
+        _lib._check_no_grad("call", a, None, b)
+    with torch.no_grad():
+        _lib._check_no_grad("call", a, b)

@@ -6,7 +6,7 @@ import torch
 
 import gated_delta_rule_157_b200 as kda
 from helpers import to_np
-from test_packed_gpu import batch, check, close, conv_batch, conv_expect
+from test_packed_gpu import batch, call, check, close, conv_batch, conv_expect
 
 pytestmark = pytest.mark.gpu
 
@@ -44,3 +44,21 @@ def test_convolution_skips_bad_bounds_only(cuda_device, cu):
     close(t["y"][once.to(cuda_device)], y[once.numpy()])
     with pytest.raises(kda.KdaError):
         kda.kda_device_status()
+
+
+def test_tensors_that_require_grad_are_refused(cuda_device):
+    """The packed calls have no backward: every floating tensor is looked at."""
+    for name in ("q", "k", "v", "g", "beta", "pool", "A_log", "dt_bias"):
+        t, kw = batch(cuda_device, [3, 2], 1, 2, 128, 128, "bf16", "bounded", False)
+        (kw if name in kw else t)[name].requires_grad_()
+        with pytest.raises(ValueError, match="no backward"):
+            call(t, kw)
+        with torch.no_grad():
+            call(t, kw)
+    for name in ("x", "w", "bias", "pool"):
+        t, kw = conv_batch(cuda_device, [3, 2], 128, 4, "bf16")
+        t[name].requires_grad_()
+        with pytest.raises(ValueError, match="no backward"):
+            kda.kda_packed_conv(t["x"], t["w"], t["pool"], t["bias"], **kw)
+        with torch.no_grad():
+            kda.kda_packed_conv(t["x"], t["w"], t["pool"], t["bias"], **kw)
