@@ -532,6 +532,12 @@ def _check_packing(cu_seqlens, slots, fresh, rows, dev):
     return n, fresh
 
 
+def _packed_out(shape, dt, dev, cu_seqlens, slots):
+    """The output that a packed call allocates: rows that it may leave out hold zeros."""
+    make = torch.empty if cu_seqlens is None and slots is None else torch.zeros
+    return make(shape, dtype=dt, device=dev)
+
+
 def _check_no_grad(name, *tensors):
     """For entry points without a backward: gradients would be lost in silence."""
     if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
@@ -551,7 +557,7 @@ def kda_packed_fwd(q, k, v, g, beta, pool, *, cu_seqlens=None, slots=None, fresh
     as they are.  pool [P,HV,Dk,Dv] float32.  cu_seqlens [N+1] int32 row bounds
     (None: every row is a sequence, a decode step); slots [N] int32 (None:
     sequence s has slot s; negative: the sequence is skipped, its rows of o left
-    as they were); fresh [N] uint8 or bool: start from a zero state.  max_seqlen:
+    as they were, or zero where o is not given); fresh [N] uint8 or bool: start from a zero state.  max_seqlen:
     the longest length if known (None: unknown), picks kernels only.  algo:
     "auto", "simt" (recurrence, fp32) or "tc" (chunks on the tensor cores: bf16,
     Dk = Dv = 128, g_per_head).  The other arguments as kda_chunk_fwd.
@@ -580,7 +586,7 @@ def kda_packed_fwd(q, k, v, g, beta, pool, *, cu_seqlens=None, slots=None, fresh
     _check(dt_bias, "dt_bias", bshape, torch.float32, dev)
     n, fresh = _check_packing(cu_seqlens, slots, fresh, T, dev)
     if o is None:
-        o = torch.empty((T, HV, Dv), dtype=dt, device=dev)
+        o = _packed_out((T, HV, Dv), dt, dev, cu_seqlens, slots)
     ld_o = _check_rows(o, "o", (T, HV, Dv), dt, dev)
     _check_no_grad("kda_packed_fwd", q, k, v, g, beta, A_log, dt_bias, pool, o)
     a = PackedArgs(n, T, P, H, HV, Dk, Dv, int(max_seqlen or 0), code, ALGOS[algo], g_min, scale, l2_eps,
@@ -612,7 +618,7 @@ def kda_packed_conv(x, w, pool, bias=None, *, cu_seqlens=None, slots=None, fresh
     _check(pool, "pool", (P, K - 1, C), dt, dev)
     n, fresh = _check_packing(cu_seqlens, slots, fresh, T, dev)
     if y is None:
-        y = torch.empty((T, C), dtype=dt, device=dev)
+        y = _packed_out((T, C), dt, dev, cu_seqlens, slots)
     ld_y = _check_rows(y, "y", (T, C), dt, dev)
     _check_no_grad("kda_packed_conv", x, w, bias, pool, y)
     a = PackedConvArgs(n, T, P, C, K, int(head_dim), bool(silu), code, l2_eps, ld_x, ld_y, x.data_ptr(), w.data_ptr(),

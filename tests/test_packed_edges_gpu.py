@@ -6,7 +6,7 @@ import torch
 
 import gated_delta_rule_157_b200 as kda
 from helpers import to_np
-from test_packed_gpu import batch, call, check, close, conv_batch, conv_expect
+from test_packed_gpu import batch, call, check, close, conv_batch, conv_expect, expect
 
 pytestmark = pytest.mark.gpu
 
@@ -62,3 +62,25 @@ def test_tensors_that_require_grad_are_refused(cuda_device):
             kda.kda_packed_conv(t["x"], t["w"], t["pool"], t["bias"], **kw)
         with torch.no_grad():
             kda.kda_packed_conv(t["x"], t["w"], t["pool"], t["bias"], **kw)
+
+
+def test_rows_that_are_left_out_of_a_new_output_are_zero(cuda_device):
+    """Skipped sequences and rows outside every sequence, where the call allocates
+    the output over memory that held something else."""
+    for per_head in (False, True):
+        t, kw = batch(cuda_device, [3, 20, 40], 1, 2, 128, 128, "bf16", "softplus", per_head, slots=[1, -1, 0], behind=7)
+        t["o"].zero_()
+        o, _ = expect(t, kw)
+        junk = torch.full_like(t["o"], float("nan"))
+        del junk
+        got = kda.kda_packed_fwd(t["q"], t["k"], t["v"], t["g"], t["beta"], t["pool"], **kw)
+        assert (got[3:23] == 0).all() and (got[63:] == 0).all()
+        close(got, o)
+    t, kw = conv_batch(cuda_device, [4, 5, 6], 128, 4, "bf16", slots=[2, -1, 0], behind=3)
+    t["y"].zero_()
+    y, _ = conv_expect(t, kw)
+    junk = torch.full_like(t["y"], float("nan"))
+    del junk
+    got = kda.kda_packed_conv(t["x"], t["w"], t["pool"], t["bias"], **kw)
+    assert (got[4:9] == 0).all() and (got[15:] == 0).all()
+    close(got, y)
