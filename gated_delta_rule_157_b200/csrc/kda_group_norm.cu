@@ -16,11 +16,14 @@
 // variance is the sum of squared distances from the mean (two sweeps over the
 // registers), so a large mean costs no digits.
 //
-// Tiled form: (1) per tile of rows and channel, mean and squared distances
-// about a pivot (forward) or sum du, sum du h (backward); (2) their sums over
-// tiles and the group's channels in a fixed order -- no atomics, the same bits
-// every run; (3) the result.  Vectors may straddle groups in (1) and (3), so D
-// is free there.
+// Tiled form: (1) per tile of rows and channel, mean and squared distances from it
+// (forward) or sum du, sum du h (backward); (2) their sums over tiles and the
+// group's channels in a fixed order -- no atomics, the same bits every run; (3) the
+// result.  Vectors may straddle groups in (1) and (3), so D is free there.  A thread
+// squares distances from the mean of four rows at a time and joins (mean, squares) of
+// two sets a, b by M2 = M2_a + M2_b + (mean_b - mean_a)^2 n_a n_b / n: no large sums are
+// subtracted, whatever the rows.  Sums stay short at any length: at most kDepth
+// steps a thread, trees over threads, compensated sums over tiles.
 //
 // Measured (bf16): 16384 rows of 32 groups of 128 with a gate 92 us, 4.4 TB/s, and
 // their gradient for 8192 rows 82 us, 4.1 TB/s; rows of 8192 x 1024 in 4 slabs,
@@ -32,6 +35,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kRows = 4;                   // rows a thread requests together
+constexpr int kDepth = 64;                 // steps a thread of the tiled form sums one after another
 extern __shared__ float smem[];
 
 template <typename Tin, int VEC> struct Vec;
@@ -354,24 +358,36 @@ gn_held_bwd_kernel(const GroupNormParams p, const GroupNormPlan pl) {
         }
 }
 
+// A sum that carries what its additions round off.  (Where it leaves the range of
+// finite values it is what it is.)
+struct LongSum {
+    float s = 0.f, lost = 0.f;
+    __device__ __forceinline__ void add(float x) {
+        const float t = s + x, v = t - s;
+        lost += (s - (t - v)) + (x - v);
+        s = t;
+    }
+    __device__ __forceinline__ float value() const { return fabsf(s) < INFINITY ? s + lost : s; }
+};
+
 // out[k][c] = sum over the `rows` partial rows ws[row][k][c], in a fixed order:
 // 32 threads per channel, each every 32nd row; block = 32 channels.
 constexpr int kSumThreads = 1024;
 __device__ __forceinline__ void sum_rows(const float *ws, int rows, int C, float *dw, float *db, int block) {
     const int c = block * 32 + (threadIdx.x & 31), part = threadIdx.x >> 5;
-    float a = 0.f, b = 0.f;
+    LongSum sa, sb;
     if (c < C) {
 #pragma unroll 4
         for (int r = part; r < rows; r += 32) {
-            a += ws[((size_t)r * 2 + 0) * C + c];
-            b += ws[((size_t)r * 2 + 1) * C + c];
+            sa.add(ws[((size_t)r * 2 + 0) * C + c]);
+            sb.add(ws[((size_t)r * 2 + 1) * C + c]);
         }
     }
-    smem[threadIdx.x] = a;
-    smem[kSumThreads + threadIdx.x] = b;
+    smem[threadIdx.x] = sa.value();
+    smem[kSumThreads + threadIdx.x] = sb.value();
     __syncthreads();
     if (part == 0 && c < C) {
-        a = b = 0.f;
+        float a = 0.f, b = 0.f;
         for (int k = 0; k < 32; ++k) {
             a += smem[32 * k + threadIdx.x];
             b += smem[kSumThreads + 32 * k + threadIdx.x];
@@ -403,49 +419,101 @@ struct TilePlace {
     }
 };
 
+// Sums of (a, b) over a column's row lanes, in its lane 0 (a tree).
+__device__ __forceinline__ void lane_sum2(float &a, float &b, const TilePlace &at, int cvb) {
+    for (int half = at.lanes >> 1; half > 0; half >>= 1) {
+        __syncthreads();
+        if (at.rl >= half && at.rl < 2 * half) {
+            smem[threadIdx.x] = a;
+            smem[kThreads + threadIdx.x] = b;
+        }
+        __syncthreads();
+        if (at.rl < half) {
+            a += smem[threadIdx.x + half * cvb];
+            b += smem[kThreads + threadIdx.x + half * cvb];
+        }
+    }
+}
+// Joins nb values of mean mb and squared distances qb to na of (mean, m2); na + nb > 0.
+__device__ __forceinline__ void join(float &mean, float &m2, float na, float mb, float qb, float nb) {
+    const float w = nb / (na + nb), d = mb - mean;
+    mean = na > 0.f ? fmaf(d, w, mean) : mb;
+    m2 = na > 0.f ? m2 + fmaf(d, d * (na * w), qb) : qb;
+}
 // ws[(n * tiles + tile)][0][c] = mean, [1][c] = sum of squared distances from it.
 template <typename Tin, int VEC>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
 gn_tile_stats_kernel(const GroupNormParams p, const GroupNormPlan pl) {
     const TilePlace at(p, pl);
     const bool in = at.cv * VEC < p.C;
     const Tin *x = static_cast<const Tin *>(p.x) + (long long)at.n * p.L * p.C + (long long)at.cv * VEC;
-    float pivot[VEC], s1[VEC], s2[VEC];
+    float mean[VEC], m2[VEC], cnt = 0.f;
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) pivot[j] = s1[j] = s2[j] = 0.f;
+    for (int j = 0; j < VEC; ++j) mean[j] = m2[j] = 0.f;
     if (in) {
-        Vec<Tin, VEC> v;
-        v.load(x + (long long)at.l0 * p.C);
-        v.get(pivot);                      // the tile's first row: the same for every row lane
-#pragma unroll 4
-        for (int l = at.l0 + at.rl; l < at.l1; l += at.lanes) {
-            float f[VEC];
-            v.load(x + (long long)l * p.C);
-            v.get(f);
+        Vec<Tin, VEC> v[kRows];
+        for (int l = at.l0 + at.rl; l < at.l1; l += kRows * at.lanes) {
+            float rows = 0.f;
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                const float d = f[j] - pivot[j];
-                s1[j] += d;
-                s2[j] = fmaf(d, d, s2[j]);
+            for (int q = 0; q < kRows; ++q) {
+                if (l + q * at.lanes >= at.l1) break;
+                v[q].load(x + (long long)(l + q * at.lanes) * p.C);
+                rows += 1.f;
             }
+            float s[VEC], sq[VEC];
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) s[j] = sq[j] = 0.f;
+#pragma unroll
+            for (int q = 0; q < kRows; ++q) {
+                if (l + q * at.lanes >= at.l1) break;
+                float f[VEC];
+                v[q].get(f);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) s[j] += f[j];
+            }
+            const float inv = 1.f / rows;
+#pragma unroll
+            for (int q = 0; q < kRows; ++q) {
+                if (l + q * at.lanes >= at.l1) break;
+                float f[VEC];
+                v[q].get(f);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    const float d = f[j] - s[j] * inv;
+                    sq[j] = fmaf(d, d, sq[j]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) join(mean[j], m2[j], cnt, s[j] * inv, sq[j], rows);
+            cnt += rows;
         }
     }
-    const float cnt = (float)(at.l1 - at.l0);
+    // the row lanes meet two by two
+    for (int half = at.lanes >> 1; half > 0; half >>= 1) {
+        float *other = smem + 2 * kThreads;
+        __syncthreads();
+        if (at.rl >= half && at.rl < 2 * half) other[threadIdx.x] = cnt;
+        __syncthreads();
+        const float nb = at.rl < half ? other[threadIdx.x + half * pl.cvb] : 0.f;
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-        __syncthreads();
-        smem[threadIdx.x] = s1[j];
-        smem[kThreads + threadIdx.x] = s2[j];
-        __syncthreads();
-        if (at.rl == 0 && in) {
-            float a = 0.f, b = 0.f;
-            for (int k = 0; k < at.lanes; ++k) {
-                a += smem[k * pl.cvb + threadIdx.x];
-                b += smem[kThreads + k * pl.cvb + threadIdx.x];
+        for (int j = 0; j < VEC; ++j) {
+            __syncthreads();
+            if (at.rl >= half && at.rl < 2 * half) {
+                smem[threadIdx.x] = mean[j];
+                smem[kThreads + threadIdx.x] = m2[j];
             }
+            __syncthreads();
+            if (nb > 0.f)
+                join(mean[j], m2[j], cnt, smem[threadIdx.x + half * pl.cvb], smem[kThreads + threadIdx.x + half * pl.cvb], nb);
+        }
+        cnt += nb;
+    }
+    if (at.rl == 0 && in) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
             float *o = p.ws + (size_t)blockIdx.x * 2 * p.C + (size_t)at.cv * VEC + j;
-            o[0] = pivot[j] + a / cnt;
-            o[p.C] = fmaxf(b - a * a / cnt, 0.f);
+            o[0] = mean[j];
+            o[p.C] = m2[j];
         }
     }
 }
@@ -457,21 +525,21 @@ gn_tile_mean_kernel(const GroupNormParams p, const GroupNormPlan pl) {
     const float *ws = p.ws + (size_t)n * pl.tiles * 2 * p.C + (size_t)g * p.D;
     const int items = pl.tiles * p.D;
     const float inv = 1.f / ((float)p.L * (float)p.D);
-    float sum = 0.f;
+    LongSum sum;
     for (int i = threadIdx.x; i < items; i += kThreads) {
         const int t = i / p.D, d = i - t * p.D;
         const float cnt = (float)(min((t + 1) * pl.rt, p.L) - t * pl.rt);
-        sum = fmaf(cnt, ws[(size_t)t * 2 * p.C + d], sum);
+        sum.add(cnt * ws[(size_t)t * 2 * p.C + d]);
     }
-    const float mean = slab_sum(sum, kThreads) * inv;
-    float m2 = 0.f;
+    const float mean = slab_sum(sum.value(), kThreads) * inv;
+    LongSum sq;
     for (int i = threadIdx.x; i < items; i += kThreads) {
         const int t = i / p.D, d = i - t * p.D;
         const float cnt = (float)(min((t + 1) * pl.rt, p.L) - t * pl.rt);
         const float e = ws[(size_t)t * 2 * p.C + d] - mean;
-        m2 += fmaf(cnt * e, e, ws[((size_t)t * 2 + 1) * p.C + d]);
+        sq.add(fmaf(cnt * e, e, ws[((size_t)t * 2 + 1) * p.C + d]));
     }
-    m2 = slab_sum(m2, kThreads);
+    const float m2 = slab_sum(sq.value(), kThreads);
     if (threadIdx.x == 0) {
         p.mean[(size_t)n * p.G + g] = mean;
         p.rstd[(size_t)n * p.G + g] = 1.f / sqrtf(fmaf(m2, inv, p.eps));
@@ -562,19 +630,11 @@ gn_tile_dsum_kernel(const GroupNormParams p, const GroupNormPlan pl) {
     }
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
-        __syncthreads();
-        smem[threadIdx.x] = sh[j];
-        smem[kThreads + threadIdx.x] = su[j];
-        __syncthreads();
+        lane_sum2(sh[j], su[j], at, pl.cvb);
         if (at.rl == 0 && in) {
-            float a = 0.f, c = 0.f;
-            for (int k = 0; k < at.lanes; ++k) {
-                a += smem[k * pl.cvb + threadIdx.x];
-                c += smem[kThreads + k * pl.cvb + threadIdx.x];
-            }
             float *o = p.ws + (size_t)blockIdx.x * 2 * p.C + (size_t)at.cv * VEC + j;
-            o[0] = a;
-            o[p.C] = c;
+            o[0] = sh[j];
+            o[p.C] = su[j];
         }
     }
 }
@@ -590,14 +650,15 @@ gn_tile_gsum_kernel(const GroupNormParams p, const GroupNormPlan pl, float *out)
     const int n = blockIdx.x / p.G, g = blockIdx.x % p.G;
     const float *ws = p.ws + (size_t)n * pl.tiles * 2 * p.C + (size_t)g * p.D;
     const int items = pl.tiles * p.D;
-    float s1 = 0.f, s2 = 0.f;
+    LongSum t1, t2;
 #pragma unroll 4
     for (int i = threadIdx.x; i < items; i += kSumThreads) {
         const int t = i / p.D, d = i - t * p.D;
         const float w = p.weight ? p.weight[g * p.D + d] : 1.f;
-        s2 = fmaf(w, ws[(size_t)t * 2 * p.C + d], s2);
-        s1 = fmaf(w, ws[((size_t)t * 2 + 1) * p.C + d], s1);
+        t2.add(w * ws[(size_t)t * 2 * p.C + d]);
+        t1.add(w * ws[((size_t)t * 2 + 1) * p.C + d]);
     }
+    float s1 = t1.value(), s2 = t2.value();
     slab_sum2(s1, s2, kSumThreads);
     if (threadIdx.x == 0) {
         const float inv = 1.f / ((float)p.L * (float)p.D);
@@ -660,7 +721,7 @@ gn_tile_bwd_kernel(const GroupNormParams p, const GroupNormPlan pl, const float 
 }
 
 constexpr size_t kHeldSmem = (64 + 2 * kThreads) * sizeof(float);
-constexpr size_t kTileSmem = 2 * kThreads * sizeof(float);
+constexpr size_t kTileSmem = 3 * kThreads * sizeof(float);
 constexpr size_t kSumSmem = 2 * kSumThreads * sizeof(float);
 
 template <typename Tin, int VEC, int VPT>
@@ -756,6 +817,9 @@ GroupNormPlan group_norm_plan(int N, int L, int C, int G, bool bf16, bool backwa
         const long long rows = ((long long)N + pl.nsub - 1) / pl.nsub;
         long long gy = slots / pl.gx;
         if (gy < 1) gy = 1;
+        // no more than 4 kDepth rows one after another in the sums of dweight and dbias
+        if (backward && gy < rows / (4 * kDepth)) gy = rows / (4 * kDepth);
+        if (gy > 65535) gy = 65535;
         if (gy > rows) gy = rows;
         pl.gy = (int)gy;
         pl.ws_floats = backward ? (size_t)pl.gy * 2 * C : 0;
@@ -767,10 +831,12 @@ GroupNormPlan group_norm_plan(int N, int L, int C, int G, bool bf16, bool backwa
     if (pl.cvb > kThreads) pl.cvb = kThreads;
     pl.gy = (cv + pl.cvb - 1) / pl.cvb;
     const int lanes = kThreads / pl.cvb;
-    // as many tiles as make one round of resident blocks, of 4 rows a thread or more
+    // as many tiles as make one round of resident blocks, of 4 rows a thread or more;
+    // no more than kDepth steps a thread (of kRows rows forward, of one backward)
     long long tiles = slots / ((long long)N * pl.gy);
     if (tiles > (L + 4 * lanes - 1) / (4 * lanes)) tiles = (L + 4 * lanes - 1) / (4 * lanes);
-    if (tiles < 1) tiles = 1;
+    const long long most = (long long)kDepth * (backward ? 1 : kRows) * lanes;
+    if (tiles < (L + most - 1) / most) tiles = (L + most - 1) / most;
     pl.rt = (int)((L + tiles - 1) / tiles);
     pl.tiles = (L + pl.rt - 1) / pl.rt;
     pl.gx = N * pl.tiles;
