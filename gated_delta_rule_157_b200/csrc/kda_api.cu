@@ -462,8 +462,18 @@ static bool group_norm_sizes(int N, int L, int C, int G, int dtype) {
     return N >= 0 && L >= 1 && C >= 1 && G >= 1 && C % G == 0 && (dtype == KDA_DT_F32 || dtype == KDA_DT_BF16);
 }
 
+// What the kernels count in an int: rows, the values of a slab and channels, with room
+// for a step beyond the last (at most 2 x 65535 x 256 rows); and the grid's limits.
+static bool group_norm_supported(int N, int L, int C, int G, int dtype, bool backward) {
+    constexpr long long most = 0x7FFFFFFFll - (1ll << 26);
+    if ((long long)N * L > most || (long long)L * (C / G) > most || (long long)N * G + C > most) return false;
+    for (int aligned = 0; N > 0 && aligned < 2; ++aligned)
+        if (kda::group_norm_plan(N, L, C, G, dtype == KDA_DT_BF16, backward, aligned != 0).gy > 65535) return false;
+    return true;
+}
+
 unsigned long long kda_group_norm_workspace(int N, int L, int C, int G, int dtype, int backward) {
-    if (!group_norm_sizes(N, L, C, G, dtype) || N == 0) return 0;
+    if (!group_norm_sizes(N, L, C, G, dtype) || N == 0 || !group_norm_supported(N, L, C, G, dtype, backward != 0)) return 0;
     const bool bf16 = dtype == KDA_DT_BF16;
     // the larger of the plans with and without 16-byte aligned pointers
     const size_t a = kda::group_norm_plan(N, L, C, G, bf16, backward != 0, true).ws_floats;
@@ -479,10 +489,7 @@ static kda_status group_norm(const kda_group_norm_args *a, void *stream, bool ba
     const bool bf16 = a->dtype == KDA_DT_BF16;
     const size_t es = bf16 ? 2 : 4;
     const size_t nx = (size_t)a->N * a->L * a->C * es, nc = (size_t)a->C * 4, ns = (size_t)a->N * a->G * 4;
-    // the grid's limit, and the element counts of a slab that the kernels keep in an int
-    if ((long long)a->N * a->L > 0x7FFFFFFFll || (long long)a->N * a->G + a->C > 0x7FFFFFFFll ||
-        (long long)a->L * (a->C / a->G) > 0x7FFFFFFFll)
-        return KDA_ERR_UNSUPPORTED;
+    if (!group_norm_supported(a->N, a->L, a->C, a->G, a->dtype, backward)) return KDA_ERR_UNSUPPORTED;
     if (backward && a->dgate && !a->gate) return KDA_ERR_INVALID_ARG;
     const float *f4[] = {a->weight, a->bias, a->mean, a->rstd, a->dweight, a->dbias};
     for (const float *p : f4)

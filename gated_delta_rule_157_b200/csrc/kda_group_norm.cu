@@ -827,8 +827,7 @@ GroupNormPlan group_norm_plan(int N, int L, int C, int G, bool bf16, bool backwa
     }
     pl.vec = aligned && C % full == 0 ? full : 1;
     const int cv = (C + pl.vec - 1) / pl.vec;
-    pl.cvb = pow2_at_least(cv);
-    if (pl.cvb > kThreads) pl.cvb = kThreads;
+    pl.cvb = cv < kThreads ? pow2_at_least(cv) : kThreads;
     pl.gy = (cv + pl.cvb - 1) / pl.cvb;
     const int lanes = kThreads / pl.cvb;
     // as many tiles as make one round of resident blocks, of 4 rows a thread or more;

@@ -433,12 +433,15 @@ typedef struct {
 } kda_group_norm_args;
 
 /* Bytes of workspace the forward (backward = 0) or the backward of these sizes
- * needs (0: none, workspace may be NULL); 0 for invalid sizes. */
+ * needs (0: none, workspace may be NULL); 0 for invalid or unsupported sizes.  A
+ * gradient with L == 1 keeps 2 C floats per block of rows, or per row where C / G
+ * channels do not fit a block (beyond 4096 bf16 or 2048 fp32 ones, 512 unaligned). */
 unsigned long long kda_group_norm_workspace(int N, int L, int C, int G, int dtype, int backward);
 
 /* Forward: writes y, mean and rstd.  Backward: writes dx and dgate in x's type,
  * dweight and dbias in fp32, summed in a fixed order (the same bits every run).
- * Any C, G with C % G == 0; activation pointers aligned to their elements
+ * Any C, G with C % G == 0; N * L, L * C / G and N * G + C up to 2^31 - 2^26 (else
+ * KDA_ERR_UNSUPPORTED, as a C beyond 65535 x 256 vectors); activation pointers aligned to their elements
  * (16-byte aligned ones are read in vectors).  No output may overlap an input,
  * another output or the workspace.  N == 0 writes zeros to dweight and dbias. */
 kda_status kda_group_norm_fwd(const kda_group_norm_args *args, void *stream);
