@@ -75,8 +75,10 @@ template <typename Tin> struct Vec<Tin, 1> {
     static __device__ __forceinline__ void put(Tin *p, const float (&f)[1]) { st_act(p, 0, f[0]); }
 };
 
-// Sigmoid: library exp and division for fp32 values; for bf16 ones the hardware
-// approximations, whose error (below 2^-20) vanishes in the rounding to 8 bits.
+// Sigmoid of a forward pass: library exp and division for fp32 values; for bf16 ones
+// the hardware approximations, off by 2^-21 of the value near 0 and by 2^-18 at |u| =
+// 88 (the product by log2 e is rounded), which vanishes in the output's rounding to
+// 8 bits.
 template <typename Tin> __device__ __forceinline__ float sig(float u) { return 1.f / (1.f + expf(-u)); }
 template <> __device__ __forceinline__ float sig<__nv_bfloat16>(float u) {
     return rcpf_(1.f + ex2f_(-kLog2E * u));
@@ -86,14 +88,15 @@ template <typename Tin> __device__ __forceinline__ float act_f(int act, float u)
     const float p = sig<Tin>(u);
     return act == 1 ? u * p : p;
 }
-// f(u) and f'(u)
-template <typename Tin> __device__ __forceinline__ void act_fd(int act, float u, float &f, float &d) {
+// f(u) and f'(u).  SUMS: for dweight and dbias, which are fp32 whatever the inputs:
+// library exp, and a reciprocal of one ulp (7 % of the one-pass gradient's time).
+template <typename Tin, bool SUMS> __device__ __forceinline__ void act_fd(int act, float u, float &f, float &d) {
     if (act == 0) {
         f = u;
         d = 1.f;
         return;
     }
-    const float p = sig<Tin>(u), r = p * (1.f - p);
+    const float p = SUMS ? rcpf_(1.f + expf(-u)) : sig<Tin>(u), r = p * (1.f - p);
     f = act == 1 ? u * p : p;
     d = act == 1 ? fmaf(u, r, p) : r;
 }
@@ -297,11 +300,11 @@ gn_held_bwd_kernel(const GroupNormParams p, const GroupNormPlan pl) {
                 const float u = fmaf(hh, w[i][j], b[i][j]);
                 float f, d, du;
                 if (GATED) {
-                    act_fd<Tin>(p.act, z[i][j], f, d);
+                    act_fd<Tin, true>(p.act, z[i][j], f, d);
                     z[i][j] = g * u * d;
                     du = g * f;
                 } else {
-                    act_fd<Tin>(p.act, u, f, d);
+                    act_fd<Tin, true>(p.act, u, f, d);
                     du = g * d;
                 }
                 dw[i][j] = fmaf(du, hh, dw[i][j]);
@@ -620,7 +623,7 @@ gn_tile_dsum_kernel(const GroupNormParams p, const GroupNormPlan pl) {
                 for (int j = 0; j < VEC; ++j) {
                     const float h = (f[j] - m[j]) * r[j];
                     float a, d;
-                    act_fd<Tin>(p.act, GATED ? z[j] : fmaf(h, w[j], b[j]), a, d);
+                    act_fd<Tin, true>(p.act, GATED ? z[j] : fmaf(h, w[j], b[j]), a, d);
                     const float du = g[j] * (GATED ? a : d);
                     su[j] += du;
                     sh[j] = fmaf(du, h, sh[j]);
@@ -709,7 +712,7 @@ gn_tile_bwd_kernel(const GroupNormParams p, const GroupNormPlan pl, const float 
             for (int j = 0; j < VEC; ++j) {
                 const float h = (f[j] - m[j]) * r[j], u = fmaf(h, w[j], b[j]);
                 float a, d;
-                act_fd<Tin>(p.act, GATED ? z[j] : u, a, d);
+                act_fd<Tin, false>(p.act, GATED ? z[j] : u, a, d);
                 const float du = g[j] * (GATED ? a : d);
                 if (GATED) z[j] = g[j] * u * d;
                 f[j] = r[j] * (fmaf(du, w[j], -s1[j]) - h * s2[j]);

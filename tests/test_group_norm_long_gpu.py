@@ -81,3 +81,22 @@ def test_overflowing_squares_leave_no_small_variance(cuda_device, N, L):
     m, r = formula(x[2:], 4, None, None)
     assert ((rstd[2:].double() - r).abs() <= F32 * r.max()).all()
     assert torch.isfinite(rstd[1, 1:]).all()
+
+
+@pytest.mark.parametrize("L", [1, 1500])
+def test_parameter_gradients_of_bf16_rows_are_fp32(cuda_device, L):
+    """dbias with one term a channel is the activated gate itself: e^-z (1 ulp), 1 + e^-z
+    (half), its reciprocal (1) and the sum with zeros -- within 3 * 2^-23 of its value.
+    (A sigmoid from a rounded -z log2 e would be off by 2^-18 far out.)"""
+    C = 1024
+    z = torch.linspace(-86.0, 86.0, C, device=cuda_device).to(torch.bfloat16)
+    x = torch.zeros(1, L, C, dtype=torch.bfloat16, device=cuda_device)
+    x[0, 0] = 1
+    dy = torch.zeros_like(x)
+    dy[0, L // 2] = 1
+    gate = z.expand(1, L, C).contiguous()
+    one, zero = torch.ones(1, 8, device=cuda_device), torch.zeros(1, 8, device=cuda_device)
+    w, b = torch.ones(C, device=cuda_device), torch.zeros(C, device=cuda_device)
+    d = kda.kda_group_norm_bwd(dy, x, 8, zero, one, w, b, gate, act="sigmoid")
+    want = torch.sigmoid(z.double())
+    assert float(((d["dbias"].double() - want) / want).abs().max()) <= 3 * 2.0 ** -23
