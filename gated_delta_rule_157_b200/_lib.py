@@ -540,8 +540,11 @@ def _packed_out(shape, dt, dev, cu_seqlens, slots):
 
 def _check_no_grad(name, *tensors):
     """For entry points without a backward: gradients would be lost in silence."""
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
-        raise ValueError("%s has no backward: call it under torch.no_grad() or on detached tensors" % name)
+    if not torch.is_grad_enabled():
+        return
+    for t in tensors:
+        if t is not None and t.requires_grad:
+            raise ValueError("%s has no backward: call it under torch.no_grad() or on detached tensors" % name)
 
 
 @_on_stream
