@@ -25,9 +25,10 @@
 // subtracted, whatever the rows.  Sums stay short at any length: at most kDepth
 // steps a thread, trees over threads, compensated sums over tiles.
 //
-// Measured (bf16): 16384 rows of 32 groups of 128 with a gate 92 us, 4.4 TB/s, and
-// their gradient for 8192 rows 82 us, 4.1 TB/s; rows of 8192 x 1024 in 4 slabs,
-// gradient 93 us: x and dy are read twice there, the second time partly from L2.
+// Measured on the device (bf16): 16384 rows of 32 groups of 128 with a gate 88 us, 4.6
+// TB/s (issue slots 77 % busy, 40 % of the warps), and their gradient for 8192 rows 84
+// us, 4.0 TB/s (issue 65 %, 24 % of the warps); rows of 8192 x 1024 in 4 slabs, gradient
+// 85 us: x and dy are read twice, from memory both times.
 #include "kda_group_norm.cuh"
 
 namespace kda {
@@ -802,7 +803,9 @@ GroupNormPlan group_norm_plan(int N, int L, int C, int G, bool bf16, bool backwa
     GroupNormPlan pl = {};
     const int D = C / G, full = bf16 ? 8 : 4;
     // blocks of 256 threads that are resident at once (registers allow four of the
-    // forward, two of the backward): more would only be more partial rows
+    // forward, two of the backward) on the 148 SMs of the one device this is built for
+    // -- a count asked of the current device could differ between the workspace's
+    // query and the call: more blocks would only be more partial rows
     const long long slots = 148ll * (backward ? 2 : 4);
     // held: vectors lie inside a group
     const int hv = aligned && D % full == 0 ? full : 1;

@@ -17,10 +17,10 @@
 // one tile of a token per warp (decode, verification) nothing is kept for a next tile, which
 // leaves registers for more blocks: there it is the traffic that counts.
 //
-// A decode step of 256 x 32 chains (1.08 GB) takes 238 us, 4.5 TB/s: the traffic,
-// with the wait for a block's first rows on top.  A ragged prefill of 6 x 16
-// chains is bound by the longest chain, 0.63 us a token: about 250 instructions
-// of each warp, most of them dependent.
+// A decode step of 256 x 32 chains (1.08 GB) takes 238 us on the device, 4.5 TB/s: the
+// traffic, with the wait for a block's first rows on top (24 % of the warps active,
+// issue slots 33 %).  A ragged prefill of 6 x 16 chains is bound by the longest chain,
+// 0.63 us a token: 283 instructions of each warp, most of them dependent.
 #include "kda_packed.cuh"
 
 namespace kda {

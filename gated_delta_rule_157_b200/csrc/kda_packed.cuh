@@ -77,8 +77,8 @@ cudaError_t launch_packed_chunk(const PackedParams &p, cudaStream_t s);
 bool packed_chunk_shape(const PackedParams &p, bool bf16);
 bool packed_chunk_aligned(const PackedParams &p);
 // Sequences of more rows than this go to the chunk kernel where it applies
-// (HV = 32, recurrence against chunks: 8 sequences of 8 rows 16 : 28 us, of 16
-// 29 : 27, of 64 81 : 27; 64 sequences of 8 rows 86 : 143 us, of 16 205 : 144).
+// (HV = 32, recurrence against chunks: 8 sequences of 8 rows 19 : 30 us, of 16
+// 29 : 30, of 64 79 : 30; 64 sequences of 8 rows 87 : 161 us, of 16 204 : 161).
 constexpr int kPackedSplit = 12;
 cudaError_t launch_packed_conv(const PackedConvParams &p, bool bf16, cudaStream_t s);
 // Error words of the packed kernels, read and cleared (after a synchronise).

@@ -11,10 +11,10 @@
 // it and writes the slot's new window, after its own read of the old one: nobody
 // else reads the slot.
 //
-// 16391 rows of 4096 channels take 75 us, 3.6 TB/s of 6.55: two special functions
-// a value (30 us of that unit alone) and 16 warps an SM, which 128 registers
-// allow.  A run is as long as leaves 16 warps an SM, 32 rows at most: a short run
-// reads K - 1 rows again.
+// 16391 rows of 4096 channels take 74 us on the device, 3.6 TB/s of 6.55: two special
+// functions a value (that unit 46 % busy, issue slots 49 %) at the 16 warps an SM that
+// 128 registers allow.  A run is as long as leaves 16 warps an SM (of the 148 of the
+// one device this is built for), 32 rows at most: a short run reads K - 1 rows again.
 #include "kda_packed.cuh"
 
 namespace kda {

@@ -46,8 +46,8 @@
 // What bounds it: the chain of one chunk, about 11,500 cycles: what is left of P 700,
 // O of the chunk before 800 and its stores 1,000, R 1,900, U 1,700, its terms for dS
 // 1,100, dS 1,500, S and its terms 1,300, their stores 1,300 (the MMAs and the warps'
-// TMEM accesses slow each other).  DRAM 12 %.  32768 rows x 32 heads in 4 sequences:
-// 0.81 ms, 1.0 TB/s.  What shortened it: shared-memory addresses formed without a
+// TMEM accesses slow each other).  The tensor pipe is 35 % busy, issue slots 47 %, DRAM
+// 12 %.  32768 rows x 32 heads in 4 sequences: 0.76 to 0.82 ms, 1.0 TB/s.  What shortened it: shared-memory addresses formed without a
 // trip through an integer (accesses had become generic ones, and registers
 // spilled), a warp that only issues, gates off the prep groups' path, no barrier
 // among the state warps, U' before U.  Measured and not kept: 4 state warps of whole

@@ -121,7 +121,7 @@ def conv_bounds(lib):
         T, n = max(x for x in cu if x <= 151), len(cu) - 1
         pack = dict(cu=cu, slots=list(range(n)), fresh=None, P=n)
         gen = torch.Generator().manual_seed(i)
-        for dtype, run in ((torch.float32, 1), (torch.bfloat16, 4), (torch.float32, 8)):
+        for dtype, run in ((torch.float32, 1), (torch.bfloat16, 4), (torch.float32, 8))[: 3 if n < 6 else 1 + i % 2]:
             C, K = 128, 4
             x, w = torch.randn(T, C, generator=gen).to(dtype), torch.randn(C, K, generator=gen)
             pool, y = torch.randn(n, K - 1, C, generator=gen).to(dtype), torch.full((T, C), 0.0625).to(dtype)
