@@ -84,3 +84,75 @@ def test_rows_that_are_left_out_of_a_new_output_are_zero(cuda_device):
     got = kda.kda_packed_conv(t["x"], t["w"], t["pool"], t["bias"], **kw)
     assert (got[4:9] == 0).all() and (got[15:] == 0).all()
     close(got, y)
+
+
+@pytest.mark.parametrize("per_head,algo", [(False, "auto"), (True, "tc"), (True, "simt")])
+def test_outputs_whose_rows_lie_apart(cuda_device, per_head, algo):
+    """o and y as columns of wider rows, whose other columns stay as they were."""
+    t, kw = batch(cuda_device, [3, 70, 1], 1, 2, 128, 128, "bf16", "softplus", per_head)
+    wide = torch.full((74, 400), 0.0625, dtype=torch.bfloat16, device=cuda_device)
+    t["o"] = wide[:, 64:320].unflatten(1, (2, 128))
+    check(t, kw, algo=algo)
+    assert (wide[:, :64] == 0.0625).all() and (wide[:, 320:] == 0.0625).all()
+    t, kw = conv_batch(cuda_device, [3, 70, 1], 256, 4, "bf16")
+    wide = torch.full((74, 400), 0.0625, dtype=torch.bfloat16, device=cuda_device)
+    y, _ = conv_expect(t, kw)
+    kda.kda_packed_conv(t["x"], t["w"], t["pool"], t["bias"], y=wide[:, 64:320], **kw)
+    close(wide[:, 64:320], y)
+    assert (wide[:, :64] == 0.0625).all() and (wide[:, 320:] == 0.0625).all()
+
+
+@pytest.mark.parametrize("per_head", [False, True])
+def test_bounds_without_slots(cuda_device, per_head):
+    """Sequence s has slot s; a pool larger than the batch keeps its other slots."""
+    t, kw = batch(cuda_device, [5, 0, 80, 1], 1, 2, 128, 128, "bf16", "softplus", per_head, P=6, slots=[0, 1, 2, 3])
+    kw["slots"] = torch.arange(4, dtype=torch.int32, device=cuda_device)
+    o, pool = expect(t, kw)
+    call(t, dict(kw, slots=None))
+    close(t["o"], o)
+    close(t["pool"], pool)
+    kda.kda_device_status()
+
+
+def test_no_rows_and_no_sequences(cuda_device):
+    """Empty batches change nothing."""
+    for lens in ([], [0, 0]):
+        t, kw = batch(cuda_device, lens, 1, 2, 128, 128, "bf16", "softplus", True, P=3)
+        kw["slots"] = torch.arange(len(lens), dtype=torch.int32, device=cuda_device)
+        before = t["pool"].clone()
+        for algo in ("auto", "simt", "tc"):
+            assert call(t, kw, algo=algo).shape == (0, 2, 128)
+        assert torch.equal(t["pool"], before)
+        c, ck = conv_batch(cuda_device, lens, 128, 4, "bf16", P=3)
+        ck["slots"] = kw["slots"]
+        before = c["pool"].clone()
+        assert kda.kda_packed_conv(c["x"], c["w"], c["pool"], c["bias"], **ck).shape == (0, 128)
+        assert torch.equal(c["pool"], before)
+    kda.kda_device_status()
+
+
+def test_two_captured_calls_share_a_pool(cuda_device):
+    """Two graphs over slots of one pool, replayed in turn and on two streams."""
+    made = [batch(cuda_device, [70, 2], 1, 2, 128, 128, "bf16", "softplus", True, seed=i, slots=[2 * i, 2 * i + 1], P=4)
+            for i in range(2)]
+    pool = made[0][0]["pool"]
+    made[1][0]["pool"] = pool
+    start = pool.clone()
+    graphs, outs = [], []
+    for t, kw in made:
+        call(t, kw)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(kda.kda_packed_fwd(t["q"], t["k"], t["v"], t["g"], t["beta"], pool, **kw))
+        graphs.append(graph)
+    pool.copy_(start)
+    want = [expect(t, kw) for t, kw in made]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for s, graph in zip(streams, graphs):
+        with torch.cuda.stream(s):
+            graph.replay()
+    torch.cuda.synchronize()
+    for i in range(2):
+        close(outs[i], want[i][0])
+        close(pool[2 * i:2 * i + 2], want[i][1][2 * i:2 * i + 2])
