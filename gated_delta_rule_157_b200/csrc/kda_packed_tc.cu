@@ -208,14 +208,13 @@ __device__ __forceinline__ void split2(float2 v, uint32_t (&w)[N]) {
         if (i + 1 < N) v = __ffma2_rn(make_float2(bf_lo(w[i]), bf_hi(w[i])), make_float2(-1.f, -1.f), v);
     }
 }
-// 16 consecutive columns of an operand row as three terms at TMEM columns, term by
-// term: eight words live at a time.
 // The leading 8 bits of both values, and what they leave.
 __device__ __forceinline__ uint32_t top2(float2 v) { return __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x7632u); }
 __device__ __forceinline__ float2 rest2(float2 v) {
     return __ffma2_rn(make_float2(bf_hi(__float_as_uint(v.x)), bf_hi(__float_as_uint(v.y))), make_float2(-1.f, -1.f), v);
 }
-// Cut off one after another: exact.
+// 16 consecutive columns of an operand row as three terms at TMEM columns, term by
+// term (eight words live at a time).  Cut off one after another: exact.
 __device__ __forceinline__ void put_cut(uint32_t at0, uint32_t at1, uint32_t at2, const float2 (&v)[8]) {
     float2 r[8];
     uint32_t w[8];
@@ -235,7 +234,7 @@ __device__ __forceinline__ void put_cut(uint32_t at0, uint32_t at1, uint32_t at2
     for (int u = 0; u < 8; ++u) w[u] = top2(r[u]);
     tmem_st8(at2, w);
 }
-// Rounded terms: two over the 16 columns themselves and a third at `third`.
+// The same with rounded terms, two over the 16 columns themselves and a third at `third`.
 __device__ __forceinline__ void put_three(uint32_t taddr, uint32_t third, const float2 (&v)[8]) {
     float2 r[8];
 #pragma unroll
